@@ -12,6 +12,8 @@ Entry points (same names as the C ABI):
   nvfp4_gemm         W4A4 GEMM C = A B^T over two K-major copies, fp32 output
   qadamw_v_encode    Q-AdamW second-moment encode (sqrt, bf16 tile mean, RHT, NVFP4)
   qadamw_v_decode    its inverse
+The MXFP4 operators (E8M0 scales per 32; dense and grouped-by-expert products) are in
+``mxfp4.py`` and re-exported here.
 """
 import ctypes
 import os
@@ -19,6 +21,11 @@ from dataclasses import dataclass
 from typing import Optional
 
 import torch
+
+from . import mxfp4 as _mxfp4
+from .mxfp4 import (MXFP4_SCALE_CEIL, MXFP4_SCALE_FLOOR, MXTensor, mxfp4_dequantize, mxfp4_gemm,
+                    mxfp4_gemm_grouped, mxfp4_gemm_grouped_wgrad, mxfp4_linear,
+                    mxfp4_linear_workspace_bytes, mxfp4_quant_params, mxfp4_quantize)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libnvfp4.so")
@@ -136,6 +143,7 @@ def load_library(path: Optional[str] = None):
     if lib.nvfp4_abi_version() != ABI_VERSION:
         raise Nvfp4Error(f"{p} has ABI version {lib.nvfp4_abi_version()}, this binding expects "
                          f"{ABI_VERSION}: rebuild the HIP library (__graft_entry__.build())")
+    _mxfp4.bind(lib)
     if path is None:
         _lib = lib
     return lib

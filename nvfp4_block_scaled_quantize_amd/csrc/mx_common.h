@@ -1,0 +1,161 @@
+// mx_common.h -- what the MXFP4 kernels share: the block scale, groups of rows, host checks.
+#pragma once
+#include "mxfp4.h"
+#include "device_common.h"
+
+namespace nvfp4 {
+
+constexpr uint32_t kTagMxSR = 0x4D585352u;
+constexpr int kMxBlock = 32;    // elements per E8M0 scale
+constexpr int kMxPad = 128;     // a copy's K extent is a multiple of this
+constexpr int64_t kMxMaxK = (int64_t)1 << 23;   // 256 rows of codes stay within 2^30 bytes
+
+inline int64_t mx_pad(int64_t k) { return (k + kMxPad - 1) / kMxPad * kMxPad; }
+
+// E8M0 code of a block from the binary32 bits of its largest magnitude (magnitudes order as
+// their bits do, infinities and NaN above every finite one).  With e the exponent field:
+// FLOOR is 2^(e - 127 - 2), code e - 2; CEIL is one more when amax > 1.5 * 2^(e - 127), i.e.
+// amax > 6 * 2^(e - 127 - 2).  Subnormal maxima have e = 0 and take code 0 (2^-127), which
+// both rules' lower bound gives: amax < 2^-126 <= 6 * 2^-127.
+template <int RULE>
+__device__ __forceinline__ uint32_t mx_scale_code(uint32_t amax_bits) {
+    uint32_t e = amax_bits >> 23;
+    if (e == 255u) return 255u;
+    if constexpr (RULE == MXFP4_SCALE_CEIL) e += (amax_bits & 0x7FFFFFu) > 0x400000u ? 1u : 0u;
+    return (e > 2u ? e : 2u) - 2u;
+}
+
+// 2^(code - 127) as binary32 for codes 0..254 (0 gives the subnormal 2^-127).
+__device__ __forceinline__ float mx_scale_value(uint32_t code) {
+    const uint32_t b = code << 23;
+    return __uint_as_float(b > 0x400000u ? b : 0x400000u);
+}
+
+// A unit (`unit` consecutive rows, or fewer at a group's end) of the rows of a grouped matrix.
+struct MxUnit {
+    int group;        // n_groups for the rows past the last group
+    int64_t row0;     // first row of the unit
+    int64_t rows;     // rows in the unit (<= unit)
+    int64_t first;    // units of the groups before this one
+    int64_t group_row0, group_rows;
+};
+
+// Blocks of a group of `rows` rows in a grouped columnwise copy.
+__device__ __forceinline__ int64_t mx_blocks(int64_t rows) {
+    return (rows + kMxPad - 1) / kMxPad * (kMxPad / kMxBlock);
+}
+
+// Inclusive scans over the wave's 64 lanes.
+__device__ __forceinline__ int wave_scan_max(int v) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int u = __shfl_up(v, o, 64);
+        if (lane >= o) v = v > u ? v : u;
+    }
+    return v;
+}
+__device__ __forceinline__ int wave_scan_add(int v) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int u = __shfl_up(v, o, 64);
+        if (lane >= o) v += u;
+    }
+    return v;
+}
+
+// Finds unit `u` of the groups' units in order (each group ceil(rows / unit) of them, then
+// those of the rows in no group); false when there are fewer.  Offsets are clamped to
+// [0, rows] and made non-decreasing.  `u` is uniform over the wave, and all 64 lanes call: a
+// lane reads one group's end, so 64 groups cost one load and two wave scans.
+__device__ __forceinline__ bool mx_find_unit(const int32_t* offsets, int n_groups, int rows, int unit,
+                                             int64_t u, MxUnit& out) {
+    const int lane = threadIdx.x & 63;
+    int end = 0;          // end of the groups before `base`
+    int64_t units = 0;    // their units
+    for (int base = 0; base < n_groups; base += 64) {
+        const int g = base + lane;
+        int e = g < n_groups ? offsets[g + 1] : 0;
+        e = e < rows ? e : rows;
+        e = e > end ? e : end;
+        e = wave_scan_max(e);
+        int s = __shfl_up(e, 1, 64);
+        s = lane ? s : end;
+        const int n = (e - s + unit - 1) / unit;
+        const int p = wave_scan_add(n);
+        const uint64_t hit = __builtin_amdgcn_ballot_w64(units + p > u);
+        if (hit) {
+            const int at = __builtin_ctzll(hit);
+            const int gs = __shfl(s, at, 64), ge = __shfl(e, at, 64);
+            out.group = base + at;
+            out.first = units + __shfl(p - n, at, 64);
+            out.group_row0 = gs;
+            out.group_rows = ge - gs;
+            out.row0 = gs + (u - out.first) * unit;
+            out.rows = ge - out.row0 < unit ? ge - out.row0 : unit;
+            return true;
+        }
+        end = __shfl(e, 63, 64);
+        units += __shfl(p, 63, 64);
+    }
+    out.group = n_groups;
+    out.first = units;
+    out.group_row0 = end;
+    out.group_rows = rows - end;
+    out.row0 = end + (u - units) * unit;
+    if (out.row0 >= rows) return false;
+    out.rows = rows - out.row0 < unit ? rows - out.row0 : unit;
+    return true;
+}
+
+// Group g's rows and the number of `unit`-row units before it.  All 64 lanes call.
+__device__ __forceinline__ void mx_group(const int32_t* offsets, int n_groups, int rows, int unit, int g,
+                                         MxUnit& out) {
+    const int lane = threadIdx.x & 63;
+    int end = 0;
+    int64_t units = 0;
+    for (int base = 0; base < n_groups; base += 64) {
+        const int q = base + lane;
+        int e = q < n_groups ? offsets[q + 1] : 0;
+        e = e < rows ? e : rows;
+        e = e > end ? e : end;
+        e = wave_scan_max(e);
+        int s = __shfl_up(e, 1, 64);
+        s = lane ? s : end;
+        const int n = (e - s + unit - 1) / unit;
+        const int p = wave_scan_add(n);
+        if (g < base + 64) {
+            const int at = g - base;
+            out.group = g;
+            out.first = units + __shfl(p - n, at, 64);
+            out.group_row0 = out.row0 = __shfl(s, at, 64);
+            out.group_rows = out.rows = __shfl(e, at, 64) - out.row0;
+            return;
+        }
+        end = __shfl(e, 63, 64);
+        units += __shfl(p, 63, 64);
+    }
+}
+
+// ---------------------------------------------------------------- host checks
+// `used`: the copy has elements, so its arrays must exist.
+inline int mx_check_tensor(const mxfp4_tensor* t, bool used) {
+    if (!t || (used && (!t->codes || !t->scales))) return NVFP4_ERR_NULL;
+    if (((uintptr_t)t->codes & 15) || ((uintptr_t)t->scales & 3)) return NVFP4_ERR_ALIGN;
+    return NVFP4_OK;
+}
+inline int mx_dtype_size(int dtype) {
+    return dtype == NVFP4_F32 ? 4 : dtype == NVFP4_BF16 ? 2 : 0;
+}
+// Groups: an offsets array goes with n_groups >= 1, none with 0; row numbers are int32.
+inline int mx_check_groups(const int32_t* offsets, int64_t n_groups, int64_t rows) {
+    if (n_groups < 0 || n_groups > 65536 || (n_groups && rows > 0x7FFFFFFF - 65536))
+        return NVFP4_ERR_SHAPE;
+    if (n_groups && !offsets) return NVFP4_ERR_NULL;
+    if (!n_groups && offsets) return NVFP4_ERR_MODE;
+    if ((uintptr_t)offsets & 3) return NVFP4_ERR_ALIGN;
+    return NVFP4_OK;
+}
+
+}  // namespace nvfp4
