@@ -145,7 +145,7 @@ def load_library(path: Optional[str] = None):
                          f"{ABI_VERSION}: rebuild the HIP library (__graft_entry__.build())")
     _mxfp4.bind(lib)
     if path is None:
-        _lib = lib
+        _lib = _mxfp4._bound = lib
     return lib
 
 

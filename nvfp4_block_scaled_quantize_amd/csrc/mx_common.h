@@ -65,6 +65,9 @@ __device__ __forceinline__ int wave_scan_add(int v) {
     return v;
 }
 
+// The value of one lane, as a scalar (the descriptors of direct loads must be scalars).
+__device__ __forceinline__ int lane_value(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
+
 // Finds unit `u` of the groups' units in order (each group ceil(rows / unit) of them, then
 // those of the rows in no group); false when there are fewer.  Offsets are clamped to
 // [0, rows] and made non-decreasing.  `u` is uniform over the wave, and all 64 lanes call: a
@@ -87,17 +90,17 @@ __device__ __forceinline__ bool mx_find_unit(const int32_t* offsets, int n_group
         const uint64_t hit = __builtin_amdgcn_ballot_w64(units + p > u);
         if (hit) {
             const int at = __builtin_ctzll(hit);
-            const int gs = __shfl(s, at, 64), ge = __shfl(e, at, 64);
+            const int gs = lane_value(s, at), ge = lane_value(e, at);
             out.group = base + at;
-            out.first = units + __shfl(p - n, at, 64);
+            out.first = units + lane_value(p - n, at);
             out.group_row0 = gs;
             out.group_rows = ge - gs;
             out.row0 = gs + (u - out.first) * unit;
             out.rows = ge - out.row0 < unit ? ge - out.row0 : unit;
             return true;
         }
-        end = __shfl(e, 63, 64);
-        units += __shfl(p, 63, 64);
+        end = lane_value(e, 63);
+        units += lane_value(p, 63);
     }
     out.group = n_groups;
     out.first = units;
@@ -107,6 +110,25 @@ __device__ __forceinline__ bool mx_find_unit(const int32_t* offsets, int n_group
     if (out.row0 >= rows) return false;
     out.rows = rows - out.row0 < unit ? rows - out.row0 : unit;
     return true;
+}
+
+// All units of the groups and of the rows in none.  All 64 lanes call.
+__device__ __forceinline__ int64_t mx_units(const int32_t* offsets, int n_groups, int rows, int unit) {
+    const int lane = threadIdx.x & 63;
+    int end = 0;
+    int64_t units = 0;
+    for (int base = 0; base < n_groups; base += 64) {
+        const int g = base + lane;
+        int e = g < n_groups ? offsets[g + 1] : 0;
+        e = e < rows ? e : rows;
+        e = e > end ? e : end;
+        e = wave_scan_max(e);
+        int s = __shfl_up(e, 1, 64);
+        s = lane ? s : end;
+        units += lane_value(wave_scan_add((e - s + unit - 1) / unit), 63);
+        end = lane_value(e, 63);
+    }
+    return units + (rows - end + unit - 1) / unit;
 }
 
 // Group g's rows and the number of `unit`-row units before it.  All 64 lanes call.
@@ -128,13 +150,13 @@ __device__ __forceinline__ void mx_group(const int32_t* offsets, int n_groups, i
         if (g < base + 64) {
             const int at = g - base;
             out.group = g;
-            out.first = units + __shfl(p - n, at, 64);
-            out.group_row0 = out.row0 = __shfl(s, at, 64);
-            out.group_rows = out.rows = __shfl(e, at, 64) - out.row0;
+            out.first = units + lane_value(p - n, at);
+            out.group_row0 = out.row0 = lane_value(s, at);
+            out.group_rows = out.rows = lane_value(e, at) - out.row0;
             return;
         }
-        end = __shfl(e, 63, 64);
-        units += __shfl(p, 63, 64);
+        end = lane_value(e, 63);
+        units += lane_value(p, 63);
     }
 }
 

@@ -8,6 +8,8 @@
 // instruction's 64 k-slots and lanes 32-63 the others.
 #include "mx_common.h"
 
+#include <atomic>
+
 namespace nvfp4 {
 
 typedef int int8v __attribute__((ext_vector_type(8)));
@@ -34,57 +36,269 @@ constexpr int kE2M1 = 4;
 __device__ __forceinline__ void store_c(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_c(uint16_t* p, float v) { *p = __builtin_bit_cast(uint16_t, (__bf16)v); }
 
-// One wave per 32 x 32 tile of C.
-template <typename T, int MODE>
-__global__ __launch_bounds__(64) void k_mx_gemm(MxGArgs g, unsigned tiles_n, unsigned tiles_m) {
-    const unsigned tn = blockIdx.x % tiles_n, tq = blockIdx.x / tiles_n;
-    const int lane = threadIdx.x, li = lane & 31, h = lane >> 5;
-    int64_t m0 = (int64_t)(tq % tiles_m) * 32, m1 = g.M, kb0 = 0, kb1 = g.kp / 32;
+// ---------------------------------------------------------------- tiled kernel
+//
+// One workgroup of four waves computes a BM x BN tile of C, wave (wm, wn) a quarter of it as
+// TM x TN accumulators of 32 x 32.  K advances in stages of 128 elements (64 code bytes a
+// row, the padding unit of the copies, so there is no partial stage).  Four stages of codes
+// are in flight in LDS; a row's scale bytes come 16 at a time, for four stages, into two
+// buffers.  All of it is written by direct global -> LDS loads: row r's four 16-byte chunks
+// lie at slots q ^ (r / 4 mod 4), which lets 16 consecutive rows' reads of one chunk touch
+// every bank once, and the loads realise that order by which chunk each lane fetches.  Rows
+// past the operand read as zeros (the loads' range check).
+//
+// A stage is two half-stages of TM x TN matrix instructions: half j multiplies chunk 2h + j
+// of every row (h: the lane's half of the wave), whose scale is byte j of the 16 bits that the
+// lane holds.  While a half-stage multiplies, the next one's fragments are read from LDS into
+// a second set of registers; the one barrier of a stage stands between its halves, and the
+// loads for three stages ahead are issued right after it.
+constexpr int kMxStage = 128, kMxStages = 4;
+constexpr int kMxScaleRows = 256;                       // rows of a scale buffer
+constexpr int kMxScaleBytes = kMxScaleRows * 16;
+
+template <int TM, int TN>
+struct MxTile {
+    static constexpr int BM = 64 * TM, BN = 64 * TN;
+    static constexpr int kA = BM * 64, kB = BN * 64;    // code bytes of a stage
+    static constexpr int kLoadsA = BM / 64, kLoadsB = BN / 64;   // per wave and stage
+    static constexpr int kLoads = kLoadsA + kLoadsB;
+    static constexpr int kScales = kMxStages * (kA + kB);        // LDS offset of the scales
+    static constexpr int kLds = kScales + 4 * kMxScaleBytes;
+};
+
+template <int N>
+__device__ __forceinline__ void wait_loads_and_barrier() {
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+// Tile id -> (tm, tn) as in the NVFP4 product: workgroups go to the eight XCDs in turn, XCD x
+// takes a contiguous range of ids, and ids walk down groups of 8 tile rows column by column,
+// so that the tiles an XCD runs at once share operand rows in its L2.
+__device__ __forceinline__ void mx_tile_of(unsigned bid, unsigned tiles_m, unsigned tiles_n, unsigned& tm,
+                                           unsigned& tn) {
+    const unsigned total = tiles_m * tiles_n, q = total / 8, r = total % 8, x = bid % 8;
+    const unsigned id = x * q + (x < r ? x : r) + bid / 8;
+    const unsigned group = id / (8 * tiles_n), first = group * 8;
+    const unsigned rows = tiles_m - first < 8 ? tiles_m - first : 8, in = id - group * 8 * tiles_n;
+    tm = first + in % rows;
+    tn = in / rows;
+}
+
+template <typename T, int MODE, int TM, int TN>
+__global__ __launch_bounds__(256, 1) void k_mx_tiles(MxGArgs g, unsigned tiles_n, unsigned tiles_m) {
+    using Tile = MxTile<TM, TN>;
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    const int t = threadIdx.x, lane = t & 63, wid = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int wm = wid >> 1, wn = wid & 1, li = lane & 31, h = lane >> 5;
+    const int64_t pitch = g.kp / 2, spitch = g.kp / 32;
+
+    // the tile: rows [m0, m1) of A and C, rows [n0, N) of B, K from k0 (in elements)
+    unsigned tm, tn;
+    int64_t m0, m1 = g.M, k0 = 0;
+    int nst = (int)(g.kp / kMxStage);
     const uint8_t *bc = g.bc, *bs = g.bs;
     T* c = (T*)g.c;
-    const int64_t pitch = g.kp / 2, spitch = g.kp / 32;
     if constexpr (MODE == MxRows) {
+        const unsigned units = (unsigned)mx_units(g.offsets, g.n_groups, (int)g.M, Tile::BM);
+        if (blockIdx.x >= units * tiles_n) return;
+        mx_tile_of(blockIdx.x, units, tiles_n, tm, tn);
         MxUnit u;
-        if (!mx_find_unit(g.offsets, g.n_groups, (int)g.M, 32, tq, u)) return;
+        mx_find_unit(g.offsets, g.n_groups, (int)g.M, Tile::BM, tm, u);
         m0 = u.row0, m1 = u.row0 + u.rows;
-        if (u.group == g.n_groups) kb1 = 0;
-        bc += u.group * g.N * pitch, bs += u.group * g.N * spitch;
+        if (u.group == g.n_groups) nst = 0;
+        else bc += u.group * g.N * pitch, bs += u.group * g.N * spitch;
     } else if constexpr (MODE == MxK) {
+        mx_tile_of(blockIdx.x, tiles_m * g.n_groups, tiles_n, tm, tn);
         MxUnit u;
-        mx_group(g.offsets, g.n_groups, (int)g.k_rows, kMxPad, (int)(tq / tiles_m), u);
-        kb0 = u.first * (kMxPad / 32), kb1 = kb0 + mx_blocks(u.rows);
+        mx_group(g.offsets, g.n_groups, (int)g.k_rows, kMxPad, (int)(tm / tiles_m), u);
+        k0 = u.first * kMxPad, nst = (int)(mx_blocks(u.rows) / (kMxPad / kMxBlock));
         c += (int64_t)u.group * g.M * g.ldc;
+        m0 = (int64_t)(tm % tiles_m) * Tile::BM;
+    } else {
+        mx_tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
+        m0 = (int64_t)tm * Tile::BM;
     }
-    const int64_t n0 = (int64_t)tn * 32;
-    const int64_t am = m0 + li < m1 ? m0 + li : m1 - 1, bn = n0 + li < g.N ? n0 + li : g.N - 1;
-    float16v acc;
+    const int64_t n0 = (int64_t)tn * Tile::BN;
+
+    float16v acc[TM][TN];
 #pragma unroll
-    for (int r = 0; r < 16; ++r) acc[r] = 0.0f;
-    for (int64_t kb = kb0 + h; kb < kb1 + h; kb += 2) {
-        const int4v a = *(const int4v*)(g.ac + am * pitch + kb * 16);
-        const int4v b = *(const int4v*)(bc + bn * pitch + kb * 16);
-        const int sa = g.as[am * spitch + kb], sb = bs[bn * spitch + kb];
-        acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(mx_frag(a), mx_frag(b), acc, kE2M1, kE2M1, 0,
-                                                              sa, 0, sb);
-    }
-    // register r of lane l is row 8 (r / 4) + 4 (l / 32) + r % 4, column l % 32
+    for (int i = 0; i < TM; ++i)
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-        const int64_t row = m0 + 8 * (r >> 2) + 4 * h + (r & 3), col = n0 + li;
-        if (row < m1 && col < g.N) store_c(c + row * g.ldc + col, acc[r]);
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+
+    if (nst > 0) {
+        const int ra = (int)(m1 - m0 < Tile::BM ? m1 - m0 : Tile::BM);
+        const int rb = (int)(g.N - n0 < Tile::BN ? g.N - n0 : Tile::BN);
+        const int4v rac = make_rsrc(g.ac + m0 * pitch + k0 / 2, (uint32_t)(ra * pitch - k0 / 2));
+        const int4v ras = make_rsrc(g.as + m0 * spitch + k0 / 32, (uint32_t)(ra * spitch - k0 / 32));
+        const int4v rbc = make_rsrc(bc + n0 * pitch + k0 / 2, (uint32_t)(rb * pitch - k0 / 2));
+        const int4v rbs = make_rsrc(bs + n0 * spitch + k0 / 32, (uint32_t)(rb * spitch - k0 / 32));
+        const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
+        // this lane's global offsets within a stage (codes) and within four stages (scales)
+        uint32_t oa[Tile::kLoadsA], ob[Tile::kLoadsB];
+#pragma unroll
+        for (int i = 0; i < Tile::kLoadsA; ++i) {
+            const int q = (wid * Tile::kLoadsA + i) * 64 + lane, row = q >> 2;
+            oa[i] = (uint32_t)(row * pitch) + (((q & 3) ^ ((row >> 2) & 3)) << 4);
+        }
+#pragma unroll
+        for (int i = 0; i < Tile::kLoadsB; ++i) {
+            const int q = (wid * Tile::kLoadsB + i) * 64 + lane, row = q >> 2;
+            ob[i] = (uint32_t)(row * pitch) + (((q & 3) ^ ((row >> 2) & 3)) << 4);
+        }
+        const uint32_t os = (uint32_t)((wid * 64 + lane) * spitch);
+
+        // load number i of stage s (an offset past the operand where there is no such stage: the
+        // count of loads in flight stays fixed)
+        const auto load_codes = [&](int s, auto ic) {
+            constexpr int i = decltype(ic)::value;
+            const uint32_t buf = lds0 + (uint32_t)(s & 3) * (Tile::kA + Tile::kB);
+            const uint32_t k = s < nst ? (uint32_t)s * 64 : kOutOfRange;
+            if constexpr (i < Tile::kLoadsA)
+                dma16(rac, buf + (uint32_t)(wid * Tile::kLoadsA + i) * 1024, oa[i] + k);
+            else
+                dma16(rbc, buf + Tile::kA + (uint32_t)(wid * Tile::kLoadsB + i - Tile::kLoadsA) * 1024,
+                      ob[i - Tile::kLoadsA] + k);
+        };
+        const auto load_scales = [&](int grp) {
+            const uint32_t buf = lds0 + Tile::kScales + (uint32_t)(grp & 1) * 2 * kMxScaleBytes + (uint32_t)wid * 1024;
+            const uint32_t k = grp * 4 < nst ? (uint32_t)grp * 16 : kOutOfRange;
+            dma16(ras, buf, os + k);
+            dma16(rbs, buf + kMxScaleBytes, os + k);
+        };
+        const auto frag = [&](int s, bool b, int tile, int j) -> int4v {
+            const int row = (b ? wn * (Tile::BN / 2) : wm * (Tile::BM / 2)) + tile * 32 + li;
+            const uint8_t* p = lds + (s & 3) * (Tile::kA + Tile::kB) + (b ? Tile::kA : 0) + row * 64 +
+                               (((2 * h + j) ^ ((row >> 2) & 3)) << 4);
+            return *(const int4v*)p;
+        };
+        const auto scale = [&](int s, bool b, int tile) -> int {
+            const int row = (b ? wn * (Tile::BN / 2) : wm * (Tile::BM / 2)) + tile * 32 + li;
+            const uint8_t* p = lds + Tile::kScales + ((s >> 2) & 1) * 2 * kMxScaleBytes +
+                               (b ? kMxScaleBytes : 0) + row * 16 + (s & 3) * 4 + 2 * h;
+            return *(const uint16_t*)p;
+        };
+
+        load_scales(0);
+        static_for<0, Tile::kLoads>([&](auto i) { load_codes(0, i); });
+        static_for<0, Tile::kLoads>([&](auto i) { load_codes(1, i); });
+        static_for<0, Tile::kLoads>([&](auto i) { load_codes(2, i); });
+        wait_loads_and_barrier<2 * Tile::kLoads>();
+
+        int4v a0[TM], b0[TN], a1[TM], b1[TN];
+        int sa[TM], sb[TN];
+#pragma unroll
+        for (int i = 0; i < TM; ++i) a0[i] = frag(0, false, i, 0), sa[i] = scale(0, false, i);
+#pragma unroll
+        for (int j = 0; j < TN; ++j) b0[j] = frag(0, true, j, 0), sb[j] = scale(0, true, j);
+
+        // Q: stage mod 4, which decides the loads in flight
+        const auto stage = [&](int s, auto qc) {
+            constexpr int Q = decltype(qc)::value;
+            int na[TM], nb[TN];
+            // first half: multiply chunk 0, read chunk 1
+            static_for<0, TM * TN>([&](auto mc) {
+                constexpr int m = decltype(mc)::value, i = m / TN, j = m % TN;
+                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                    mx_frag(a0[i]), mx_frag(b0[j]), acc[i][j], kE2M1, kE2M1, 0, sa[i], 0, sb[j]);
+                if constexpr (m < TN) b1[m] = frag(s, true, m, 1);
+                else if constexpr (m < TM + TN) a1[m - TN] = frag(s, false, m - TN, 1);
+                __builtin_amdgcn_sched_barrier(0);
+            });
+            // stage s + 1 has landed; in flight: stage s + 2, and the scales issued a stage (Q 1)
+            // or two stages (Q 2) ago
+            wait_loads_and_barrier<Tile::kLoads + (Q == 1 || Q == 2 ? 2 : 0)>();
+            // second half: multiply chunk 1; issue the loads of stage s + 3 and read chunk 0 of s + 1
+            static_for<0, TM * TN>([&](auto mc) {
+                constexpr int m = decltype(mc)::value, i = m / TN, j = m % TN;
+                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                    mx_frag(a1[i]), mx_frag(b1[j]), acc[i][j], kE2M1, kE2M1, 1, sa[i], 1, sb[j]);
+                constexpr int every = TM * TN / Tile::kLoads;
+                if constexpr (m % every == every - 1) load_codes(s + 3, std::integral_constant<int, m / every>{});
+                if constexpr (m < TN) b0[m] = frag(s + 1, true, m, 0), nb[m] = scale(s + 1, true, m);
+                else if constexpr (m < TM + TN)
+                    a0[m - TN] = frag(s + 1, false, m - TN, 0), na[m - TN] = scale(s + 1, false, m - TN);
+                __builtin_amdgcn_sched_barrier(0);
+            });
+            if constexpr (TM * TN < Tile::kLoads || TM * TN < TM + TN)
+                static_assert(TM * TN >= TM + TN && TM * TN >= Tile::kLoads, "a half-stage hides its loads");
+            if constexpr (Q == 0) load_scales(s / 4 + 1);
+#pragma unroll
+            for (int i = 0; i < TM; ++i) sa[i] = na[i];
+#pragma unroll
+            for (int j = 0; j < TN; ++j) sb[j] = nb[j];
+        };
+        int s = 0;
+        for (; s + 4 <= nst; s += 4) {
+            stage(s, std::integral_constant<int, 0>{});
+            stage(s + 1, std::integral_constant<int, 1>{});
+            stage(s + 2, std::integral_constant<int, 2>{});
+            stage(s + 3, std::integral_constant<int, 3>{});
+        }
+        if (s < nst) stage(s, std::integral_constant<int, 0>{}), ++s;
+        if (s < nst) stage(s, std::integral_constant<int, 1>{}), ++s;
+        if (s < nst) stage(s, std::integral_constant<int, 2>{});
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no load may write LDS after the wave's end
     }
+
+    // register r of lane l is row 8 (r / 4) + 4 (l / 32) + r % 4, column l % 32 of its 32 x 32
+    const int64_t row0 = m0 + wm * (Tile::BM / 2) + 4 * h, col0 = n0 + wn * (Tile::BN / 2) + li;
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const int64_t row = row0 + i * 32 + 8 * (r >> 2) + (r & 3);
+            if (row < m1)
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+                    if (col0 + j * 32 < g.N) store_c(c + row * g.ldc + col0 + j * 32, acc[i][j][r]);
+        }
+}
+
+// Lets a kernel use `bytes` of LDS, once per device (a bit of `ready` each).
+static int allow_lds(const void* kernel, int bytes, std::atomic<uint64_t>& ready) {
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess) return NVFP4_ERR_HIP;
+    const uint64_t bit = (uint64_t)1 << (dev & 63);
+    if (dev < 64 && (ready.load(std::memory_order_relaxed) & bit)) return NVFP4_OK;
+    if (hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes) != hipSuccess)
+        return NVFP4_ERR_HIP;
+    ready.fetch_or(bit, std::memory_order_relaxed);
+    return NVFP4_OK;
+}
+
+template <typename T, int MODE, int TM, int TN>
+static int launch_tiles(const MxGArgs& g, hipStream_t st) {
+    using Tile = MxTile<TM, TN>;
+    const int64_t tn = (g.N + Tile::BN - 1) / Tile::BN, tm = (g.M + Tile::BM - 1) / Tile::BM;
+    int64_t tiles = tm * tn;
+    // every group, and the rows in none, may end in a partial tile
+    if (MODE == MxRows) tiles = (g.M / Tile::BM + (g.n_groups < g.M ? g.n_groups : g.M) + 1) * tn;
+    if (MODE == MxK) tiles *= g.n_groups;
+    static_assert(Tile::kLds <= 160 * 1024, "LDS budget");
+    const auto kernel = k_mx_tiles<T, MODE, TM, TN>;
+    static std::atomic<uint64_t> ready{0};
+    if (int rc = allow_lds((const void*)kernel, Tile::kLds, ready)) return rc;
+    kernel<<<dim3((unsigned)tiles), 256, Tile::kLds, st>>>(g, (unsigned)tn, (unsigned)tm);
+    return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
 }
 
 template <int MODE>
 static int launch_gemm(const MxGArgs& g, int c_dtype, hipStream_t st) {
-    const int64_t tn = (g.N + 31) / 32;
-    int64_t tm = (g.M + 31) / 32, tiles = tm * tn;
-    if (MODE == MxRows) tiles = (g.M / 32 + (g.n_groups < g.M ? g.n_groups : g.M) + 1) * tn;
-    if (MODE == MxK) tiles *= g.n_groups;
-    const dim3 grid((unsigned)tiles);
-    if (c_dtype == NVFP4_BF16) k_mx_gemm<uint16_t, MODE><<<grid, 64, 0, st>>>(g, (unsigned)tn, (unsigned)tm);
-    else k_mx_gemm<float, MODE><<<grid, 64, 0, st>>>(g, (unsigned)tn, (unsigned)tm);
-    return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
+    const int64_t groups = MODE == MxK ? g.n_groups : 1;
+    const int64_t big = ((g.M + 255) / 256) * ((g.N + 255) / 256) * groups;
+    const int64_t small = ((g.M + 127) / 128) * ((g.N + 127) / 128) * groups;
+    // A full round of 256 tiles of 128 x 128 takes 0.46 of the time of one of 256 x 256 (15 and
+    // 31 us at K = 4096), so the smaller tile wins where it wastes less of the last round:
+    // 2048 x 2048 x 4096 15 against 31 us, 1024 x 6144 x 4096 24 against 31; but 4096^3 52
+    // against 43 and 8192^3 378 against 284.
+    if (((small + 255) / 256) * 46 < ((big + 255) / 256) * 100)
+        return c_dtype == NVFP4_BF16 ? launch_tiles<uint16_t, MODE, 2, 2>(g, st)
+                                     : launch_tiles<float, MODE, 2, 2>(g, st);
+    return c_dtype == NVFP4_BF16 ? launch_tiles<uint16_t, MODE, 4, 4>(g, st)
+                                 : launch_tiles<float, MODE, 4, 4>(g, st);
 }
 
 // Checks shared by the products; *empty when C has no elements.

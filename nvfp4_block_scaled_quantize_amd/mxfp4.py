@@ -70,9 +70,14 @@ def bind(lib):
                      f"expects {MXFP4_ABI_VERSION}: rebuild it (__graft_entry__.build())")
 
 
+_bound = None   # the package's library once it is loaded
+
+
 def _lib():
-    from . import load_library
-    return load_library()
+    if _bound is None:
+        from . import load_library
+        load_library()
+    return _bound
 
 
 def _check(rc):
@@ -80,8 +85,9 @@ def _check(rc):
         raise _error(f"nvfp4 status {rc}: {_lib().nvfp4_status_string(rc).decode()}")
 
 
-def _stream(device):
-    return torch.cuda.current_stream(device).cuda_stream
+# The current stream's handle by device index: a call of these operators can be shorter than
+# building the torch.cuda.Stream object that would otherwise carry it (0.1 against 1.9 us).
+_stream = torch._C._cuda_getCurrentRawStream
 
 
 @dataclass
@@ -120,22 +126,30 @@ def grouped_k(rows, n_groups):
     return (rows + min(rows, n_groups) * 127) // 128 * 128
 
 
-def _operand(t, name, device=None):
-    """Checks a copy's tensors; a kernel reads them by their extents alone."""
-    codes, scales = t.codes, t.scales
-    if not (codes.is_cuda and scales.is_cuda):
+def _device(t):
+    """Device index of a CUDA tensor."""
+    d = t.get_device()
+    if d < 0:
         raise _error("mxfp4 kernels take GPU tensors only (no CPU path)")
-    kp = grouped_k(t.k, t.n_groups) if t.n_groups else padded_k(t.k)
+    return d
+
+
+def _operand(t, name, device):
+    """Checks a copy's tensors (a kernel reads them by their extents alone); returns them as the
+    C struct and the codes' shape."""
+    codes, scales, k = t.codes, t.scales, t.k
+    if codes.get_device() != device or scales.get_device() != device:
+        _device(codes), _device(scales)
+        raise _error(f"{name} is on another device")
+    shape = codes.shape
+    kp = (k + 127) // 128 * 128 if not t.n_groups else grouped_k(k, t.n_groups)
+    if len(shape) < 2 or shape[-1] * 2 != kp or scales.shape != (*shape[:-1], kp // 32):
+        raise _error(f"{name}: codes {tuple(shape)} and scales {tuple(scales.shape)} do not "
+                     f"hold rows of k = {k}")
     if codes.dtype != torch.uint8 or scales.dtype != torch.uint8 or not codes.is_contiguous() \
             or not scales.is_contiguous():
         raise _error(f"{name}: codes and scales must be contiguous uint8 tensors")
-    if codes.dim() < 2 or codes.shape[-1] * 2 != kp or scales.shape[-1] * 32 != kp \
-            or codes.shape[:-1] != scales.shape[:-1]:
-        raise _error(f"{name}: codes {tuple(codes.shape)} and scales {tuple(scales.shape)} do not "
-                     f"hold rows of k = {t.k}")
-    if scales.device != codes.device or (device is not None and codes.device != device):
-        raise _error(f"{name} is on another device")
-    return MXTensorC(codes.data_ptr(), scales.data_ptr())
+    return MXTensorC(codes.data_ptr(), scales.data_ptr()), shape
 
 
 def _groups(offsets, device):
@@ -143,38 +157,44 @@ def _groups(offsets, device):
     if offsets is None:
         return None, 0
     if offsets.dtype != torch.int32 or offsets.dim() != 1 or not offsets.is_contiguous() \
-            or offsets.device != device or offsets.numel() < 2:
+            or offsets.get_device() != device or offsets.numel() < 2:
         raise _error("offsets must be a contiguous 1-D int32 tensor of n_groups + 1 >= 2 entries "
                      "on the operands' device")
     return offsets.data_ptr(), offsets.numel() - 1
 
 
 def _matrix(x, name):
-    if not x.is_cuda:
-        raise _error("mxfp4 kernels take GPU tensors only (no CPU path)")
-    if x.dtype not in _DTYPES:
+    """(device index, shape, dtype code, row pitch) of a matrix or a stack of them whose rows
+    may be views of wider ones."""
+    dtype = _DTYPES.get(x.dtype)
+    if dtype is None:
         raise _error(f"unsupported dtype {x.dtype}")
-    if x.shape[-1] > 1 and x.stride(-1) != 1:
+    device, shape = _device(x), x.shape
+    if len(shape) < 2:
+        raise _error(f"{name} must be a matrix")
+    rows, cols = shape[-2:]
+    strides = x.stride()
+    if cols > 1 and strides[-1] != 1:
         raise _error(f"{name} must have unit column stride")
+    pitch = strides[-2]
+    if pitch < cols:
+        if rows > 1:
+            raise _error(f"{name}'s rows overlap (row stride below the number of columns)")
+        pitch = cols
+    return device, shape, dtype, pitch
 
 
-def _pitch(x):
-    """Row pitch of a matrix whose rows may be views of wider ones."""
-    pitch, cols = x.stride(-2), x.shape[-1]
-    if x.shape[-2] > 1 and pitch < cols:
-        raise _error("rows overlap (row stride below the number of columns)")
-    return max(pitch, cols)
-
-
-def _output(out, shape, dtype, device):
+def _output(out, shape, dtype, like):
+    """(out, dtype code, row pitch), allocated on `like`'s device unless given."""
     if out is None:
-        if dtype not in _DTYPES:
+        code = _DTYPES.get(dtype)
+        if code is None:
             raise _error(f"unsupported dtype {dtype}")
-        return torch.empty(shape, dtype=dtype, device=device)
-    if tuple(out.shape) != tuple(shape) or out.device != device:
-        raise _error(f"out must be a {tuple(shape)} tensor on the operands' device")
-    _matrix(out, "out")
-    return out
+        return torch.empty(shape, dtype=dtype, device=like.device), code, shape[-1]
+    device, got, code, pitch = _matrix(out, "out")
+    if got != shape or device != like.get_device():
+        raise _error(f"out must be a {shape} tensor on the operands' device")
+    return out, code, pitch
 
 
 def mxfp4_quant_params(rowwise=True, colwise=False, scale_rule=MXFP4_SCALE_FLOOR, round_row=0,
@@ -189,105 +209,102 @@ def mxfp4_quantize(x, params, offsets=None, row_out=None, col_out=None):
     strides, unit column stride).  Returns (row_copy, col_copy), None for one not requested: the
     rowwise copy [.., rows][cols] and the columnwise copy [.., cols][rows].  With offsets (2-D x
     only) the columnwise copy's blocks restart at each group of rows."""
-    _matrix(x, "x")
-    if x.dim() not in (2, 3):
+    dev, shape, dtype, pitch = _matrix(x, "x")
+    if len(shape) > 3:
         raise _error("x must be a 2-D or 3-D tensor")
-    dev = x.device
     op, groups = _groups(offsets, dev)
-    if groups and x.dim() != 2:
+    if groups and len(shape) != 2:
         raise _error("grouped rows need a 2-D x")
-    R, C = x.shape[-2:]
-    batch = x.shape[0] if x.dim() == 3 else 1
-    lead = (batch,) if x.dim() == 3 else ()
-    row = col = None
+    R, C = shape[-2:]
+    lead = tuple(shape[:-2])
+    batch = lead[0] if lead else 1
+    row = col = rc = cc = None
     if params.rowwise:
-        row = row_out if row_out is not None else MXTensor.empty((*lead, R), C, dev)
-        rc = _operand(row, "row_out", dev)
-        if row.shape != (*lead, R, C) or row.n_groups:
-            raise _error(f"row_out {row.shape} does not hold x {tuple(x.shape)}")
+        row = row_out if row_out is not None else MXTensor.empty((*lead, R), C, x.device)
+        rc, got = _operand(row, "row_out", dev)
+        if got[:-1] != (*lead, R) or row.k != C or row.n_groups:
+            raise _error(f"row_out {row.shape} does not hold x {tuple(shape)}")
     if params.colwise:
-        col = col_out if col_out is not None else MXTensor.empty((*lead, C), R, dev, groups)
-        cc = _operand(col, "col_out", dev)
-        if col.shape != (*lead, C, R) or col.n_groups != groups:
-            raise _error(f"col_out {col.shape} does not hold x {tuple(x.shape)} transposed")
-    _check(_lib().mxfp4_quantize(x.data_ptr(), _DTYPES[x.dtype], batch, R, C, _pitch(x),
-                                 x.stride(0) if batch > 1 else 0, op, groups, params,
-                                 rc if row is not None else None, cc if col is not None else None,
+        col = col_out if col_out is not None else MXTensor.empty((*lead, C), R, x.device, groups)
+        cc, got = _operand(col, "col_out", dev)
+        if got[:-1] != (*lead, C) or col.k != R or col.n_groups != groups:
+            raise _error(f"col_out {col.shape} does not hold x {tuple(shape)} transposed")
+    _check(_lib().mxfp4_quantize(x.data_ptr(), dtype, batch, R, C, pitch,
+                                 x.stride(0) if batch > 1 else 0, op, groups, params, rc, cc,
                                  _stream(dev)))
     return row, col
 
 
 def mxfp4_dequantize(q, out_dtype=torch.float32, offsets=None, out=None):
     """The values of a copy, [.., n][k]; a grouped columnwise copy takes its offsets."""
-    qc = _operand(q, "q")
-    dev = q.codes.device
+    dev = _device(q.codes)
+    qc, shape = _operand(q, "q", dev)
     op, groups = _groups(offsets, dev)
     if groups != q.n_groups:
         raise _error(f"the copy has {q.n_groups} groups, offsets {groups}")
-    out = _output(out, q.shape, out_dtype, dev)
-    if out.dim() > 2 and not out.is_contiguous():
-        raise _error("out of a stack of matrices must be contiguous")
-    n = 1
-    for d in q.codes.shape[:-1]:
-        n *= d
-    _check(_lib().mxfp4_dequantize(qc, n, q.k, op, groups, _DTYPES[out.dtype], out.data_ptr(),
-                                   _pitch(out), _stream(dev)))
+    out, dtype, pitch = _output(out, (*shape[:-1], q.k), out_dtype, q.codes)
+    n = shape[0]
+    if len(shape) > 2:
+        if not out.is_contiguous():
+            raise _error("out of a stack of matrices must be contiguous")
+        for d in shape[1:-1]:
+            n *= d
+    _check(_lib().mxfp4_dequantize(qc, n, q.k, op, groups, dtype, out.data_ptr(), pitch, _stream(dev)))
     return out
 
 
 def mxfp4_gemm(a, b, out=None, out_dtype=torch.float32):
     """C = A B^T (A: M x K copy, B: N x K copy)."""
-    ac = _operand(a, "a")
-    dev = a.codes.device
-    bc = _operand(b, "b", dev)
-    if a.codes.dim() != 2 or b.codes.dim() != 2 or a.n_groups or b.n_groups:
+    dev = _device(a.codes)
+    ac, sa = _operand(a, "a", dev)
+    bc, sb = _operand(b, "b", dev)
+    if len(sa) != 2 or len(sb) != 2 or a.n_groups or b.n_groups:
         raise _error("mxfp4_gemm takes two plain copies")
-    M, N = a.codes.shape[0], b.codes.shape[0]
     if a.k != b.k:
         raise _error(f"K mismatch {a.k} vs {b.k}")
-    out = _output(out, (M, N), out_dtype, dev)
-    _check(_lib().mxfp4_gemm(ac, bc, M, N, a.k, out.data_ptr(), _DTYPES[out.dtype], _pitch(out),
-                             _stream(dev)))
+    M, N = sa[0], sb[0]
+    out, dtype, pitch = _output(out, (M, N), out_dtype, a.codes)
+    _check(_lib().mxfp4_gemm(ac, bc, M, N, a.k, out.data_ptr(), dtype, pitch, _stream(dev)))
     return out
 
 
 def mxfp4_gemm_grouped(a, b, offsets, out=None, out_dtype=torch.float32):
     """C's rows of group g = A's rows of group g times B[g]^T (A: M x K copy, B: [n_groups] of
     N x K copies).  Rows in no group give 0."""
-    ac = _operand(a, "a")
-    dev = a.codes.device
-    bc = _operand(b, "b", dev)
+    dev = _device(a.codes)
+    ac, sa = _operand(a, "a", dev)
+    bc, sb = _operand(b, "b", dev)
     op, groups = _groups(offsets, dev)
-    if a.codes.dim() != 2 or b.codes.dim() != 3 or a.n_groups or b.n_groups:
+    if len(sa) != 2 or len(sb) != 3 or a.n_groups or b.n_groups:
         raise _error("mxfp4_gemm_grouped takes a copy of a matrix and one of a stack of matrices")
-    if b.codes.shape[0] != groups:
-        raise _error(f"{b.codes.shape[0]} matrices for {groups} groups")
-    M, N = a.codes.shape[0], b.codes.shape[1]
+    if sb[0] != groups:
+        raise _error(f"{sb[0]} matrices for {groups} groups")
     if a.k != b.k:
         raise _error(f"K mismatch {a.k} vs {b.k}")
-    out = _output(out, (M, N), out_dtype, dev)
-    _check(_lib().mxfp4_gemm_grouped(ac, bc, op, groups, M, N, a.k, out.data_ptr(),
-                                     _DTYPES[out.dtype], _pitch(out), _stream(dev)))
+    M, N = sa[0], sb[1]
+    out, dtype, pitch = _output(out, (M, N), out_dtype, a.codes)
+    _check(_lib().mxfp4_gemm_grouped(ac, bc, op, groups, M, N, a.k, out.data_ptr(), dtype, pitch,
+                                     _stream(dev)))
     return out
 
 
 def mxfp4_gemm_grouped_wgrad(a, b, offsets, out=None, out_dtype=torch.float32):
     """C[g] = A_g B_g^T over group g's span of two grouped columnwise copies (A: [M][rows],
     B: [N][rows]); returns [n_groups][M][N], 0 for an empty group."""
-    ac = _operand(a, "a")
-    dev = a.codes.device
-    bc = _operand(b, "b", dev)
+    dev = _device(a.codes)
+    ac, sa = _operand(a, "a", dev)
+    bc, sb = _operand(b, "b", dev)
     op, groups = _groups(offsets, dev)
-    if a.codes.dim() != 2 or b.codes.dim() != 2 or a.n_groups != groups or b.n_groups != groups:
+    if len(sa) != 2 or len(sb) != 2 or a.n_groups != groups or b.n_groups != groups or not groups:
         raise _error("mxfp4_gemm_grouped_wgrad takes two columnwise copies made with these offsets")
     if a.k != b.k:
         raise _error(f"row mismatch {a.k} vs {b.k}")
-    M, N = a.codes.shape[0], b.codes.shape[0]
-    out = _output(out, (groups, M, N), out_dtype, dev)
+    M, N = sa[0], sb[0]
+    out, dtype, _ = _output(out, (groups, M, N), out_dtype, a.codes)
     if not out.is_contiguous():
         raise _error("out must be contiguous")
-    _check(_lib().mxfp4_gemm_grouped_wgrad(ac, bc, op, groups, M, N, a.k, out.data_ptr(),
-                                           _DTYPES[out.dtype], N, _stream(dev)))
+    _check(_lib().mxfp4_gemm_grouped_wgrad(ac, bc, op, groups, M, N, a.k, out.data_ptr(), dtype, N,
+                                           _stream(dev)))
     return out
 
 
@@ -299,27 +316,25 @@ def mxfp4_linear(x, w, offsets=None, scale_rule=MXFP4_SCALE_FLOOR, out=None, out
                  workspace=None):
     """Y = Q(x) W^T: x [M][K] bf16/fp32 is quantized rowwise on the way (w: N x K copy, or, with
     offsets, a stack of one per group).  out_dtype: x's unless given."""
-    _matrix(x, "x")
-    if x.dim() != 2:
+    dev, shape, xdtype, xpitch = _matrix(x, "x")
+    if len(shape) != 2:
         raise _error("x must be a 2-D tensor")
-    dev = x.device
-    wc = _operand(w, "w", dev)
+    wc, sw = _operand(w, "w", dev)
     op, groups = _groups(offsets, dev)
-    if w.codes.dim() != (3 if groups else 2) or w.n_groups or (groups and w.codes.shape[0] != groups):
+    if len(sw) != (3 if groups else 2) or w.n_groups or (groups and sw[0] != groups):
         raise _error("w must be one copy, or with offsets a stack of one copy per group")
-    M, K = x.shape
-    N = w.codes.shape[-2]
+    M, K = shape
+    N = sw[-2]
     if w.k != K:
         raise _error(f"K mismatch {K} vs {w.k}")
-    out = _output(out, (M, N), out_dtype or x.dtype, dev)
+    out, dtype, pitch = _output(out, (M, N), out_dtype or x.dtype, x)
     lib = _lib()
     if workspace is None:
         need = lib.mxfp4_linear_workspace_bytes(M, N, K, groups)
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    elif workspace.device != dev or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        workspace = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
+    elif workspace.get_device() != dev or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise _error("workspace must be a contiguous uint8 tensor on x's device")
     ws, ws_bytes = (workspace.data_ptr(), workspace.numel()) if workspace is not None else (None, 0)
-    _check(lib.mxfp4_linear(x.data_ptr(), _DTYPES[x.dtype], M, K, _pitch(x), scale_rule, wc, N, op,
-                            groups, out.data_ptr(), _DTYPES[out.dtype], _pitch(out), ws, ws_bytes,
-                            _stream(dev)))
+    _check(lib.mxfp4_linear(x.data_ptr(), xdtype, M, K, xpitch, scale_rule, wc, N, op, groups,
+                            out.data_ptr(), dtype, pitch, ws, ws_bytes, _stream(dev)))
     return out
