@@ -16,12 +16,13 @@ inline int64_t mx_pad(int64_t k) { return (k + kMxPad - 1) / kMxPad * kMxPad; }
 // their bits do, infinities and NaN above every finite one).  With e the exponent field:
 // FLOOR is 2^(e - 127 - 2), code e - 2; CEIL is one more when amax > 1.5 * 2^(e - 127), i.e.
 // amax > 6 * 2^(e - 127 - 2).  Subnormal maxima have e = 0 and take code 0 (2^-127), which
-// both rules' lower bound gives: amax < 2^-126 <= 6 * 2^-127.
-template <int RULE>
-__device__ __forceinline__ uint32_t mx_scale_code(uint32_t amax_bits) {
+// both rules' lower bound gives: amax < 2^-126 <= 6 * 2^-127.  `above`: the largest fraction
+// field that does not round up, kMxCeilAbove or kMxFloorAbove.
+constexpr uint32_t kMxCeilAbove = 0x400000u, kMxFloorAbove = 0x7FFFFFu;
+__device__ __forceinline__ uint32_t mx_scale_code(uint32_t amax_bits, uint32_t above) {
     uint32_t e = amax_bits >> 23;
     if (e == 255u) return 255u;
-    if constexpr (RULE == MXFP4_SCALE_CEIL) e += (amax_bits & 0x7FFFFFu) > 0x400000u ? 1u : 0u;
+    e += (amax_bits & 0x7FFFFFu) > above ? 1u : 0u;
     return (e > 2u ? e : 2u) - 2u;
 }
 
@@ -158,6 +159,19 @@ __device__ __forceinline__ void mx_group(const int32_t* offsets, int n_groups, i
         end = lane_value(e, 63);
         units += lane_value(p, 63);
     }
+}
+
+// Tile id -> (tm, tn) as in the NVFP4 product: workgroups go to the eight XCDs in turn, XCD x
+// takes a contiguous range of ids, and ids walk down groups of 8 tile rows column by column,
+// so that the tiles an XCD runs at once share operand rows (and output lines) in its L2.
+__device__ __forceinline__ void mx_tile_of(unsigned bid, unsigned tiles_m, unsigned tiles_n, unsigned& tm,
+                                           unsigned& tn) {
+    const unsigned total = tiles_m * tiles_n, q = total / 8, r = total % 8, x = bid % 8;
+    const unsigned id = x * q + (x < r ? x : r) + bid / 8;
+    const unsigned group = id / (8 * tiles_n), first = group * 8;
+    const unsigned rows = tiles_m - first < 8 ? tiles_m - first : 8, in = id - group * 8 * tiles_n;
+    tm = first + in % rows;
+    tn = in / rows;
 }
 
 // ---------------------------------------------------------------- host checks

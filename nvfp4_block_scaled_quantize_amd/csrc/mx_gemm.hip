@@ -71,19 +71,6 @@ __device__ __forceinline__ void wait_loads_and_barrier() {
     asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
-// Tile id -> (tm, tn) as in the NVFP4 product: workgroups go to the eight XCDs in turn, XCD x
-// takes a contiguous range of ids, and ids walk down groups of 8 tile rows column by column,
-// so that the tiles an XCD runs at once share operand rows in its L2.
-__device__ __forceinline__ void mx_tile_of(unsigned bid, unsigned tiles_m, unsigned tiles_n, unsigned& tm,
-                                           unsigned& tn) {
-    const unsigned total = tiles_m * tiles_n, q = total / 8, r = total % 8, x = bid % 8;
-    const unsigned id = x * q + (x < r ? x : r) + bid / 8;
-    const unsigned group = id / (8 * tiles_n), first = group * 8;
-    const unsigned rows = tiles_m - first < 8 ? tiles_m - first : 8, in = id - group * 8 * tiles_n;
-    tm = first + in % rows;
-    tn = in / rows;
-}
-
 template <typename T, int MODE, int TM, int TN>
 __global__ __launch_bounds__(256, 1) void k_mx_tiles(MxGArgs g, unsigned tiles_n, unsigned tiles_m) {
     using Tile = MxTile<TM, TN>;

@@ -1,7 +1,11 @@
 // mx_quantize.hip -- MXFP4 quantization and its inverse.
 //
 // x_hat = E2M1(x / s) s with s = 2^(code - 127) from the block's largest magnitude (32
-// elements).  Division by s is exact, so the only rounding is E2M1's.
+// elements).  Division by s is exact, so the only rounding is E2M1's.  The conversion
+// instructions take s as an operand (its exponent) and bfloat16 pairs as they are.
+//
+// Bound by memory: an element costs 2 or 4 bytes read and 17/32 written per copy.  There is no
+// pass for a tensor maximum, so every element is read once.
 #include "mx_common.h"
 
 namespace nvfp4 {
@@ -11,90 +15,263 @@ struct MxQArgs {
     int64_t batch, rows, cols, ld, stride;
     const int32_t* offsets;
     int n_groups;
-    uint8_t *rc, *rs, *cc, *cs;
-    int64_t row_kp, col_kp;     // K extents of the two copies
-    uint32_t k0, k1;            // Philox key
+    uint8_t *rc, *rs, *cc, *cs;     // rc / cc null: no such copy
+    int64_t row_kp, col_kp;         // K extents of the two copies
+    uint32_t above;                 // the scale rule, see mx_scale_code
+    int sr_row, sr_col;             // stochastic rounding
+    uint32_t k0, k1;                // Philox key
 };
 
-// ROUND: NVFP4_RNE or NVFP4_SR.  Quantizes one block of 32 values and stores its 16 code bytes
-// and its scale; e0: index of the block's first element (a multiple of 32).
-template <int RULE, int ROUND>
-__device__ __forceinline__ void quantize_block(const float (&v)[32], uint8_t* codes, uint8_t* scale,
-                                               int64_t e0, uint32_t copy, uint32_t k0, uint32_t k1) {
+// Eight consecutive elements of a block.
+template <typename T> struct Oct;
+template <> struct Oct<uint16_t> { uint32_t w[4]; };
+template <> struct Oct<float> { float v[8]; };
+
+// Loads of any alignment: rows may start at any element, and the hardware splits what
+// straddles.  left: elements up to the row's end (may be <= 0); the rest are zeros.
+template <typename T>
+__device__ __forceinline__ Oct<T> load_oct(const T* p, int64_t left) {
+    Oct<T> o;
+    if (left >= 8) {
+        __builtin_memcpy(&o, p, sizeof(o));
+    } else {
+        T e[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) e[i] = i < left ? p[i] : (T)0;
+        __builtin_memcpy(&o, e, sizeof(o));
+    }
+    return o;
+}
+
+typedef unsigned short ushort2v __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2v __attribute__((ext_vector_type(2)));
+
+// Magnitude bits of two packed bfloat16 each: they order as the values do.
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(ushort2v, a),
+                                                                  __builtin_bit_cast(ushort2v, b)));
+}
+
+// binary32 bits of the largest magnitude
+__device__ __forceinline__ uint32_t max_bits(const Oct<uint16_t>& o) {
+    uint32_t m = o.w[0] & 0x7FFF7FFFu;
+#pragma unroll
+    for (int i = 1; i < 4; ++i) m = max_bf16x2(m, o.w[i] & 0x7FFF7FFFu);
+    return max(m << 16, m & 0xFFFF0000u);
+}
+__device__ __forceinline__ uint32_t max_bits(const Oct<float>& o) {
     uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-    const uint32_t code = mx_scale_code<RULE>(m);
-    const float cs = mx_scale_value(code);
-    uint32_t w[4];
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(o.v[i]) & 0x7FFFFFFFu);
+    return m;
+}
+
+__device__ __forceinline__ float value(const Oct<uint16_t>& o, int i) {
+    return __uint_as_float((i & 1) ? o.w[i >> 1] & 0xFFFF0000u : o.w[i >> 1] << 16);
+}
+__device__ __forceinline__ float value(const Oct<float>& o, int i) { return o.v[i]; }
+
+// Nearest even: eight codes of o / cs (cs a power of two).
+__device__ __forceinline__ uint32_t codes_rne(const Oct<uint16_t>& o, float cs) {
+    uint32_t w = 0;
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf16x2v, o.w[0]), cs, 0);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf16x2v, o.w[1]), cs, 1);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf16x2v, o.w[2]), cs, 2);
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf16x2v, o.w[3]), cs, 3);
+}
+__device__ __forceinline__ uint32_t codes_rne(const Oct<float>& o, float cs) {
+    uint32_t w = 0;
+    w = cvt_fp4x2<0>(w, o.v[0], o.v[1], cs);
+    w = cvt_fp4x2<1>(w, o.v[2], o.v[3], cs);
+    w = cvt_fp4x2<2>(w, o.v[4], o.v[5], cs);
+    return cvt_fp4x2<3>(w, o.v[6], o.v[7], cs);
+}
+
+// Stochastic: x / s in binary32 (exact but for results below 2^-126, which round to 0 with
+// every draw that f 2^16 < 1 allows), then the conversion at unit scale.  e: the first
+// element's index in the copy (a multiple of 8).
+template <typename T>
+__device__ __forceinline__ uint32_t codes_sr(const Oct<T>& o, uint32_t code, int64_t e, uint32_t copy,
+                                             uint32_t k0, uint32_t k1) {
+    const U4 c = {(uint32_t)(e >> 3), (uint32_t)(e >> 35), copy, kTagMxSR};
+    const U4 r = philox10(c, k0, k1);
+    const uint32_t rw[4] = {r.x, r.y, r.z, r.w};
+    const float inv = __uint_as_float((254u - code) << 23);
+    uint32_t w = 0;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        uint32_t word = 0;
-        if constexpr (ROUND == NVFP4_RNE) {
-            word = cvt_fp4x2<0>(word, v[8 * q + 0], v[8 * q + 1], cs);
-            word = cvt_fp4x2<1>(word, v[8 * q + 2], v[8 * q + 3], cs);
-            word = cvt_fp4x2<2>(word, v[8 * q + 4], v[8 * q + 5], cs);
-            word = cvt_fp4x2<3>(word, v[8 * q + 6], v[8 * q + 7], cs);
-        } else {
-            const U4 c = {(uint32_t)((e0 >> 3) + q), (uint32_t)(((e0 >> 3) + q) >> 32), copy, kTagMxSR};
-            const U4 r = philox10(c, k0, k1);
-            const uint32_t rw[4] = {r.x, r.y, r.z, r.w};
-            // x / s in binary32 (exact but for results below 2^-126, which round to 0 either
-            // way), then the conversion at unit scale
-            const float inv = __uint_as_float((254u - code) << 23);
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t bits = (i & 1) ? rw[i >> 1] & 0xFFFF0000u : rw[i >> 1] << 16;
+        w |= (cvt_fp4_sr(value(o, i) * inv, bits) & 0xFu) << (4 * i);
+    }
+    return w;
+}
+
+// SR: the kernel may round stochastically (then `sr` decides).
+template <bool SR, typename T>
+__device__ __forceinline__ uint32_t codes_of(const Oct<T>& o, uint32_t code, bool sr, int64_t e, uint32_t copy,
+                                             const MxQArgs& g) {
+    uint32_t w;
+    if (SR && sr) w = codes_sr(o, code, e, copy, g.k0, g.k1);
+    else w = codes_rne(o, mx_scale_value(code));
+    return code == 255u ? 0u : w;
+}
+
+// DPP moves within quads and within rows of 16 lanes.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
+}
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kRor4 = 0x124, kRor8 = 0x128;
+
+// Largest over the four lanes of a quad, which hold one block.
+__device__ __forceinline__ uint32_t quad_max(uint32_t m) {
+    m = max(m, dpp<kXor1>(m));
+    return max(m, dpp<kXor2>(m));
+}
+
+// Rowwise copy alone: a lane per eight elements, a quad per block, so that loads and stores
+// are contiguous over the wave.  A workgroup takes kRowSteps times 256 consecutive octs of the
+// copy (rows padded to row_kp), all loaded before the first is used.
+constexpr int kRowSteps = 4;
+template <typename T, bool SR>
+__global__ __launch_bounds__(256) void k_mx_rows(MxQArgs g) {
+    const uint32_t per = (uint32_t)(g.row_kp / 8);      // octs of a row
+    const int64_t first = (int64_t)blockIdx.x * (256 * kRowSteps), total = g.batch * g.rows * per;
+    const int64_t row0 = first / per;
+    const uint32_t rem = (uint32_t)(first - row0 * per);
+    Oct<T> o[kRowSteps];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint32_t bits = (i & 1) ? rw[i >> 1] & 0xFFFF0000u : rw[i >> 1] << 16;
-                word |= (cvt_fp4_sr(v[8 * q + i] * inv, bits) & 0xFu) << (4 * i);
+    for (int i = 0; i < kRowSteps; ++i) {
+        const uint32_t at = rem + threadIdx.x + 256 * i, dr = at / per;
+        const int64_t r = row0 + dr, k = (int64_t)(at - dr * per) * 8;
+        const int64_t b = g.batch == 1 ? 0 : r / g.rows;
+        const bool in = first + threadIdx.x + 256 * i < total;
+        o[i] = load_oct((const T*)g.x + b * g.stride + (r - b * g.rows) * g.ld + k, in ? g.cols - k : 0);
+    }
+#pragma unroll
+    for (int i = 0; i < kRowSteps; ++i) {
+        const int64_t at = first + threadIdx.x + 256 * i;   // oct of the copy
+        const uint32_t code = mx_scale_code(quad_max(max_bits(o[i])), g.above);
+        const uint32_t w = codes_of<SR>(o[i], code, g.sr_row, at * 8, 0, g);
+        if (at < total) {
+            ((uint32_t*)g.rc)[at] = w;
+            if ((threadIdx.x & 3) == 0) g.rs[at >> 2] = (uint8_t)code;
+        }
+    }
+}
+
+// Both copies, or the columnwise one: a workgroup takes a 128-row unit times 256 bytes of
+// columns (128 bfloat16, 64 float32).  Rows are loaded a lane per oct, quantized rowwise from
+// registers, and put into LDS as dwords [row][64]; then a thread takes one dword column (two
+// bfloat16 columns or one float32 one) of 32 rows.  Dword c of row r lies at c ^ 16 (r / 32), so
+// that the four row blocks of 16 dword columns, which a wave reads at once (a quad of lanes
+// per column, for 64 contiguous bytes of its codes), are in different banks.
+template <typename T, bool SR>
+__global__ __launch_bounds__(256) void k_mx_tile(MxQArgs g, unsigned units, unsigned col_tiles) {
+    constexpr int kTileCols = 256 / sizeof(T), kPerRow = kTileCols / 8;   // octs of a tile row
+    constexpr int kRowsAtOnce = 256 / kPerRow, kSteps = kMxPad / kRowsAtOnce;
+    __shared__ __attribute__((aligned(16))) uint32_t tile[kMxPad * 64];
+    const int t = threadIdx.x;
+    unsigned u, ct;
+    int64_t b = 0, row0, rows, kp0;
+    bool has_col = g.cc != nullptr;
+    if (g.n_groups) {
+        const unsigned n = (unsigned)mx_units(g.offsets, g.n_groups, (int)g.rows, kMxPad);
+        if (blockIdx.x >= n * col_tiles) return;
+        mx_tile_of(blockIdx.x, n, col_tiles, u, ct);
+        MxUnit m;
+        mx_find_unit(g.offsets, g.n_groups, (int)g.rows, kMxPad, u, m);
+        row0 = m.row0, rows = m.rows, kp0 = (int64_t)u * kMxPad;
+        if (m.group == g.n_groups) has_col = false;
+    } else {
+        mx_tile_of(blockIdx.x, units * (unsigned)g.batch, col_tiles, u, ct);
+        b = u / units, u = u % units;
+        row0 = kp0 = (int64_t)u * kMxPad;
+        rows = g.rows - row0 < kMxPad ? g.rows - row0 : kMxPad;
+    }
+    const int64_t c0 = (int64_t)ct * kTileCols;
+    const int tr = t / kPerRow, tc = t % kPerRow;        // this lane's row and oct of a step
+    const int64_t left = g.cols - c0 - tc * 8;
+    const T* p = (const T*)g.x + b * g.stride + (row0 + tr) * g.ld + c0 + tc * 8;
+    Oct<T> o[kSteps];
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i)
+        o[i] = load_oct(p + (int64_t)i * kRowsAtOnce * g.ld, tr + i * kRowsAtOnce < rows ? left : 0);
+    if (has_col) {
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            const int r = tr + i * kRowsAtOnce;
+            uint32_t* d = tile + r * 64 + ((tc * (int)sizeof(T) * 2) ^ (16 * (r >> 5)));
+            const uint4* src = (const uint4*)&o[i];
+#pragma unroll
+            for (int q = 0; q < (int)sizeof(T) / 2; ++q) ((uint4*)d)[q] = src[q];
+        }
+    }
+    if (g.rc) {
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            const int r = tr + i * kRowsAtOnce;
+            const uint32_t code = mx_scale_code(quad_max(max_bits(o[i])), g.above);
+            const int64_t e = (b * g.rows + row0 + r) * g.row_kp + c0 + tc * 8;
+            const uint32_t w = codes_of<SR>(o[i], code, g.sr_row, e, 0, g);
+            // the scale bytes of the four blocks in 16 lanes: of one bfloat16 row, or of two
+            // float32 rows, in one store a row
+            uint32_t sc = code << (8 * ((t >> 2) & 3));
+            sc |= dpp<kRor4>(sc);
+            sc |= dpp<kRor8>(sc);
+            if (r < rows) {
+                *(uint32_t*)(g.rc + e / 2) = w;
+                if (tc == 0) {
+                    if constexpr (sizeof(T) == 2) *(uint32_t*)(g.rs + e / 32) = sc;
+                    else *(uint16_t*)(g.rs + e / 32) = (uint16_t)(sc >> (8 * ((t >> 2) & 2)));
+                }
             }
         }
-        w[q] = code == 255u ? 0u : word;
     }
-    *(uint4*)codes = make_uint4(w[0], w[1], w[2], w[3]);
-    *scale = (uint8_t)code;
-}
-
-template <typename T> __device__ __forceinline__ float load_value(const T* p);
-template <> __device__ __forceinline__ float load_value<float>(const float* p) { return *p; }
-template <> __device__ __forceinline__ float load_value<uint16_t>(const uint16_t* p) {
-    return bf16_to_f32(*p);
-}
-
-// One thread per block of the rowwise copy.
-template <typename T, int RULE, int ROUND>
-__global__ void k_mx_rows(MxQArgs g) {
-    const int64_t per = g.row_kp / kMxBlock;
-    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (i >= g.batch * g.rows * per) return;
-    const int64_t r = i / per, k = (i - r * per) * kMxBlock;
-    const T* p = (const T*)g.x + r / g.rows * g.stride + r % g.rows * g.ld + k;
-    float v[32];
+    if (!has_col) return;
+    __syncthreads();
+    // dword column dc, rows 32 rb .. 32 rb + 31
+    const int rb = t & 3, dc = t >> 2;
+    const uint32_t* s = tile + rb * 32 * 64 + (dc ^ (16 * rb));
+    uint32_t d[32];
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = k + j < g.cols ? load_value(p + j) : 0.0f;
-    quantize_block<RULE, ROUND>(v, g.rc + i * 16, g.rs + i, r * g.row_kp + k, 0, g.k0, g.k1);
-}
-
-// One thread per column of a 128-row unit of the columnwise copy.
-template <typename T, int RULE, int ROUND>
-__global__ void k_mx_cols(MxQArgs g, int64_t units, unsigned col_blocks) {
-    const unsigned cb = blockIdx.x % col_blocks, ub = blockIdx.x / col_blocks;
-    const int64_t b = ub / units, u = ub % units;
-    int64_t row0 = u * kMxPad, rows = g.rows - row0, kp0 = u * kMxPad;
-    if (g.n_groups) {
-        MxUnit m;
-        if (!mx_find_unit(g.offsets, g.n_groups, (int)g.rows, kMxPad, u, m) || m.group == g.n_groups)
-            return;
-        row0 = m.row0, rows = m.rows;
+    for (int j = 0; j < 32; ++j) d[j] = s[j * 64];
+    constexpr int kCols = 4 / sizeof(T);
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+        if constexpr (sizeof(T) == 2) m = max_bf16x2(m, d[j] & 0x7FFF7FFFu);
+        else m = max(m, d[j] & 0x7FFFFFFFu);
     }
-    const int64_t c = (int64_t)cb * blockDim.x + threadIdx.x;
-    if (c >= g.cols) return;
-    const T* p = (const T*)g.x + b * g.stride + row0 * g.ld + c;
-    for (int q = 0; q < kMxPad / kMxBlock; ++q) {
-        float v[32];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = q * 32 + j < rows ? load_value(p + (q * 32 + j) * g.ld) : 0.0f;
-        const int64_t e = (b * g.cols + c) * g.col_kp + kp0 + q * 32;
-        quantize_block<RULE, ROUND>(v, g.cc + e / 2, g.cs + e / 32, e, 1, g.k0, g.k1);
+    for (int q = 0; q < kCols; ++q) {
+        const uint32_t bits = sizeof(T) == 4 ? m : q ? m & 0xFFFF0000u : m << 16;
+        const uint32_t code = mx_scale_code(bits, g.above);
+        const int64_t c = c0 + dc * kCols + q;
+        const int64_t e = (b * g.cols + c) * g.col_kp + kp0 + rb * 32;
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            Oct<T> v;
+            if constexpr (sizeof(T) == 2) {
+                // the two halves of rows j and j + 1 that belong to column q
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    v.w[j] = __builtin_amdgcn_perm(d[8 * k + 2 * j + 1], d[8 * k + 2 * j],
+                                                   q ? 0x07060302u : 0x05040100u);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v.v[j] = __uint_as_float(d[8 * k + j]);
+            }
+            w[k] = codes_of<SR>(v, code, g.sr_col, e + 8 * k, 1, g);
+        }
+        uint32_t sc = code << (8 * rb);
+        sc |= dpp<kXor1>(sc);
+        sc |= dpp<kXor2>(sc);
+        if (c < g.cols) {
+            *(uint4*)(g.cc + e / 2) = make_uint4(w[0], w[1], w[2], w[3]);
+            if (rb == 0) *(uint32_t*)(g.cs + e / 32) = sc;
+        }
     }
 }
 
@@ -107,60 +284,87 @@ struct MxDArgs {
     int64_t ld;
 };
 
-__device__ __forceinline__ void store_value(float* p, float v) { *p = v; }
-__device__ __forceinline__ void store_value(uint16_t* p, float v) {
-    // exact for copies of bf16 values; nearest even otherwise
-    *p = __builtin_bit_cast(uint16_t, (__bf16)v);
-}
-
-// One thread per 8 elements; a workgroup decodes 16 rows of a 128-wide unit of K.
+// Eight decoded elements, of which the first `left` are stored (any alignment).  bfloat16: exact
+// for copies of bfloat16 values, nearest even otherwise.
 template <typename T>
-__global__ void k_mx_decode(MxDArgs g, unsigned units) {
-    const int64_t u = blockIdx.x % units;
-    int64_t k0 = u * kMxPad, left = g.k - k0;
-    bool zero = false;
-    if (g.n_groups) {
-        MxUnit m;
-        if (!mx_find_unit(g.offsets, g.n_groups, (int)g.k, kMxPad, u, m)) return;
-        k0 = m.row0, left = m.rows, zero = m.group == g.n_groups;
-    }
-    const int64_t r = (int64_t)(blockIdx.x / units) * 16 + (threadIdx.x >> 4);
-    const int j = (int)(threadIdx.x & 15) * 8;
-    if (r >= g.n || j >= left) return;
-    const int64_t e = r * g.kp + u * kMxPad + j;
-    uint32_t w = 0, code = 0;
-    if (!zero) w = *(const uint32_t*)(g.codes + e / 2), code = g.scales[e / 32];
+__device__ __forceinline__ void decode_oct(uint32_t w, uint32_t code, T* p, int64_t left) {
     const float s = code == 255u ? __builtin_nanf("") : mx_scale_value(code);
-    const float2v p[4] = {fp4x2_to_f32<0>(w), fp4x2_to_f32<1>(w), fp4x2_to_f32<2>(w), fp4x2_to_f32<3>(w)};
-    T* o = (T*)g.out + r * g.ld + k0 + j;
+    const float2v v[4] = {fp4x2_to_f32<0>(w), fp4x2_to_f32<1>(w), fp4x2_to_f32<2>(w), fp4x2_to_f32<3>(w)};
+    T e[8];
 #pragma unroll
-    for (int q = 0; q < 8; ++q)
-        if (j + q < left) store_value(o + q, p[q >> 1][q & 1] * s);
+    for (int i = 0; i < 8; ++i) {
+        const float f = v[i >> 1][i & 1] * s;
+        if constexpr (sizeof(T) == 2) e[i] = __builtin_bit_cast(uint16_t, (__bf16)f);
+        else e[i] = f;
+    }
+    if (left >= 8) __builtin_memcpy(p, e, sizeof(e));
+    else
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < left) p[i] = e[i];
 }
 
-template <typename T, int RULE, int ROUND>
-static void launch_rows(const MxQArgs& g, hipStream_t st) {
-    const int64_t n = g.batch * g.rows * (g.row_kp / kMxBlock);
-    k_mx_rows<T, RULE, ROUND><<<dim3((unsigned)((n + 255) / 256)), 256, 0, st>>>(g);
-}
-template <typename T, int RULE, int ROUND>
-static void launch_cols(const MxQArgs& g, hipStream_t st) {
-    const int64_t units = g.col_kp / kMxPad;
-    const int64_t col_blocks = (g.cols + 255) / 256;
-    k_mx_cols<T, RULE, ROUND><<<dim3((unsigned)(col_blocks * units * g.batch)), 256, 0, st>>>(
-        g, units, (unsigned)col_blocks);
+// Plain copy: a lane per eight elements, as k_mx_rows.
+template <typename T>
+__global__ __launch_bounds__(256) void k_mx_decode(MxDArgs g) {
+    const uint32_t per = (uint32_t)(g.kp / 8);
+    const int64_t first = (int64_t)blockIdx.x * (256 * kRowSteps), total = g.n * per;
+    const int64_t row0 = first / per;
+    const uint32_t rem = (uint32_t)(first - row0 * per);
+    uint32_t w[kRowSteps], code[kRowSteps];
+#pragma unroll
+    for (int i = 0; i < kRowSteps; ++i) {
+        const int64_t at = first + threadIdx.x + 256 * i;
+        w[i] = at < total ? ((const uint32_t*)g.codes)[at] : 0u;
+        code[i] = at < total ? g.scales[at >> 2] : 0u;
+    }
+#pragma unroll
+    for (int i = 0; i < kRowSteps; ++i) {
+        const uint32_t at = rem + threadIdx.x + 256 * i, dr = at / per;
+        const int64_t r = row0 + dr, k = (int64_t)(at - dr * per) * 8;
+        if (first + threadIdx.x + 256 * i < total)
+            decode_oct(w[i], code[i], (T*)g.out + r * g.ld + k, g.k - k);
+    }
 }
 
-template <typename T, int RULE>
-static void launch_quantize(const MxQArgs& g, const mxfp4_quant_params* p, hipStream_t st) {
-    if (p->rowwise) {
-        if (p->round_row == NVFP4_RNE) launch_rows<T, RULE, NVFP4_RNE>(g, st);
-        else launch_rows<T, RULE, NVFP4_SR>(g, st);
+// Grouped columnwise copy: a workgroup takes a 128-row unit's positions of 64 of the copy's
+// rows, 16 lanes per row.
+constexpr int kDecodeSteps = 4;
+template <typename T>
+__global__ __launch_bounds__(256) void k_mx_decode_grouped(MxDArgs g, unsigned units) {
+    const int64_t u = blockIdx.x % units;
+    MxUnit m;
+    if (!mx_find_unit(g.offsets, g.n_groups, (int)g.k, kMxPad, u, m)) return;
+    const bool in = m.group != g.n_groups;
+    const int64_t row0 = (int64_t)(blockIdx.x / units) * (16 * kDecodeSteps) + (threadIdx.x >> 4);
+    const int j = (int)(threadIdx.x & 15) * 8;
+    uint32_t w[kDecodeSteps], code[kDecodeSteps];
+#pragma unroll
+    for (int i = 0; i < kDecodeSteps; ++i) {
+        const int64_t r = row0 + 16 * i, e = r * g.kp + u * kMxPad + j;
+        const bool ok = in && r < g.n;
+        w[i] = ok ? *(const uint32_t*)(g.codes + e / 2) : 0u;
+        code[i] = ok ? g.scales[e / 32] : 0u;
     }
-    if (p->colwise) {
-        if (p->round_col == NVFP4_RNE) launch_cols<T, RULE, NVFP4_RNE>(g, st);
-        else launch_cols<T, RULE, NVFP4_SR>(g, st);
+#pragma unroll
+    for (int i = 0; i < kDecodeSteps; ++i) {
+        const int64_t r = row0 + 16 * i;
+        if (r < g.n) decode_oct(w[i], code[i], (T*)g.out + r * g.ld + m.row0 + j, m.rows - j);
     }
+}
+
+template <typename T, bool SR>
+static void launch_quantize(const MxQArgs& g, hipStream_t st) {
+    if (!g.cc) {
+        const int64_t octs = g.batch * g.rows * (g.row_kp / 8), per = 256 * kRowSteps;
+        k_mx_rows<T, SR><<<dim3((unsigned)((octs + per - 1) / per)), 256, 0, st>>>(g);
+        return;
+    }
+    // units cover the rows in no group too (one more partial unit at most); tiles cover the
+    // rowwise copy's padding
+    const unsigned units = (unsigned)(g.col_kp / kMxPad), col_tiles = (unsigned)(g.row_kp * sizeof(T) / 256);
+    const int64_t grid = (g.n_groups ? units + 1 : units * g.batch) * (int64_t)col_tiles;
+    k_mx_tile<T, SR><<<dim3((unsigned)grid), 256, 0, st>>>(g, units, col_tiles);
 }
 
 }  // namespace nvfp4
@@ -208,13 +412,11 @@ extern "C" int mxfp4_quantize(const void* x, int dtype, int64_t batch, int64_t r
     if (p->colwise) g.cc = col_out->codes, g.cs = col_out->scales;
     g.k0 = (uint32_t)p->seed, g.k1 = (uint32_t)(p->seed >> 32);
     const hipStream_t st = (hipStream_t)stream;
-    const bool ceil = p->scale_rule == MXFP4_SCALE_CEIL;
-    if (dtype == NVFP4_BF16)
-        ceil ? launch_quantize<uint16_t, MXFP4_SCALE_CEIL>(g, p, st)
-             : launch_quantize<uint16_t, MXFP4_SCALE_FLOOR>(g, p, st);
-    else
-        ceil ? launch_quantize<float, MXFP4_SCALE_CEIL>(g, p, st)
-             : launch_quantize<float, MXFP4_SCALE_FLOOR>(g, p, st);
+    g.above = p->scale_rule == MXFP4_SCALE_CEIL ? kMxCeilAbove : kMxFloorAbove;
+    g.sr_row = p->round_row == NVFP4_SR, g.sr_col = p->round_col == NVFP4_SR;
+    const bool sr = (g.rc && g.sr_row) || (g.cc && g.sr_col);
+    if (dtype == NVFP4_BF16) sr ? launch_quantize<uint16_t, true>(g, st) : launch_quantize<uint16_t, false>(g, st);
+    else sr ? launch_quantize<float, true>(g, st) : launch_quantize<float, false>(g, st);
     return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
 }
 
@@ -231,11 +433,18 @@ extern "C" int mxfp4_dequantize(const mxfp4_tensor* q, int64_t n, int64_t k, con
     if ((uintptr_t)out % size) return NVFP4_ERR_ALIGN;
     MxDArgs g = {q->codes, q->scales, n, k, n_groups ? mxfp4_grouped_k(k, n_groups) : mx_pad(k),
                  offsets, (int)n_groups, out, ld_out};
-    // one unit more than the copy holds: the rows in no group
-    const unsigned units = (unsigned)(g.kp / kMxPad + (n_groups ? 1 : 0));
-    const dim3 grid((unsigned)((n + 15) / 16 * units));
     const hipStream_t st = (hipStream_t)stream;
-    if (out_dtype == NVFP4_BF16) k_mx_decode<uint16_t><<<grid, 256, 0, st>>>(g, units);
-    else k_mx_decode<float><<<grid, 256, 0, st>>>(g, units);
+    if (n_groups) {
+        // one unit more than the copy holds: the rows in no group
+        const unsigned units = (unsigned)(g.kp / kMxPad + 1);
+        const dim3 grid((unsigned)((n + 16 * kDecodeSteps - 1) / (16 * kDecodeSteps) * units));
+        if (out_dtype == NVFP4_BF16) k_mx_decode_grouped<uint16_t><<<grid, 256, 0, st>>>(g, units);
+        else k_mx_decode_grouped<float><<<grid, 256, 0, st>>>(g, units);
+    } else {
+        const int64_t octs = n * (g.kp / 8), per = 256 * kRowSteps;
+        const dim3 grid((unsigned)((octs + per - 1) / per));
+        if (out_dtype == NVFP4_BF16) k_mx_decode<uint16_t><<<grid, 256, 0, st>>>(g);
+        else k_mx_decode<float><<<grid, 256, 0, st>>>(g);
+    }
     return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
 }
