@@ -46,88 +46,87 @@ __device__ __forceinline__ int64_t mx_blocks(int64_t rows) {
     return (rows + kMxPad - 1) / kMxPad * (kMxPad / kMxBlock);
 }
 
-// Inclusive scans over the wave's 64 lanes.
-__device__ __forceinline__ int wave_scan_max(int v) {
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const int u = __shfl_up(v, o, 64);
-        if (lane >= o) v = v > u ? v : u;
-    }
-    return v;
+// DPP moves: quads, rows of 16 lanes, whole wave.  Lanes without a source (or masked rows)
+// take `old`.
+template <int CTRL, int ROWS = 0xF>
+__device__ __forceinline__ int dpp(int old, int v) {
+    return __builtin_amdgcn_update_dpp(old, v, CTRL, ROWS, 0xF, false);
 }
-__device__ __forceinline__ int wave_scan_add(int v) {
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const int u = __shfl_up(v, o, 64);
-        if (lane >= o) v += u;
-    }
-    return v;
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kRor4 = 0x124, kRor8 = 0x128, kWaveShr1 = 0x138;
+
+// Inclusive scan over the wave's 64 lanes of non-negative values: within rows of 16, then the
+// last lane of rows 0 and 2 into rows 1 and 3, then lane 31 into the upper half.
+template <typename Op>
+__device__ __forceinline__ int wave_scan(int v, Op op) {
+    v = op(v, dpp<0x111>(0, v));
+    v = op(v, dpp<0x112>(0, v));
+    v = op(v, dpp<0x114>(0, v));
+    v = op(v, dpp<0x118>(0, v));
+    v = op(v, dpp<0x142, 0xA>(0, v));
+    return op(v, dpp<0x143, 0xC>(0, v));
 }
 
 // The value of one lane, as a scalar (the descriptors of direct loads must be scalars).
 __device__ __forceinline__ int lane_value(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
 
-// Finds unit `u` of the groups' units in order (each group ceil(rows / unit) of them, then
-// those of the rows in no group); false when there are fewer.  Offsets are clamped to
-// [0, rows] and made non-decreasing.  `u` is uniform over the wave, and all 64 lanes call: a
-// lane reads one group's end, so 64 groups cost one load and two wave scans.
-__device__ __forceinline__ bool mx_find_unit(const int32_t* offsets, int n_groups, int rows, int unit,
-                                             int64_t u, MxUnit& out) {
-    const int lane = threadIdx.x & 63;
+// 64 consecutive groups, one per lane: rows [s, e), their units n and the inclusive count p of
+// units.  Offsets are clamped to [0, rows] and made non-decreasing.
+struct MxSpan {
+    int s, e, n, p;
+};
+__device__ __forceinline__ MxSpan mx_span(const int32_t* offsets, int n_groups, int rows, int unit, int base,
+                                          int end) {
+    const int g = base + (threadIdx.x & 63);
+    int e = g < n_groups ? offsets[g + 1] : 0;
+    e = e < rows ? e : rows;
+    e = e > end ? e : end;
+    MxSpan x;
+    x.e = wave_scan(e, [](int a, int b) { return a > b ? a : b; });
+    x.s = dpp<kWaveShr1>(end, x.e);
+    x.n = (x.e - x.s + unit - 1) / unit;
+    x.p = wave_scan(x.n, [](int a, int b) { return a + b; });
+    return x;
+}
+
+// Unit `u` of the groups' units in order (each group ceil(rows / unit) of them, then those of
+// the rows in no group), which exists.  `u` is uniform over the wave; all 64 lanes call.
+__device__ __forceinline__ void mx_find_unit(const int32_t* offsets, int n_groups, int rows, int unit, int64_t u,
+                                             MxUnit& out) {
     int end = 0;          // end of the groups before `base`
     int64_t units = 0;    // their units
     for (int base = 0; base < n_groups; base += 64) {
-        const int g = base + lane;
-        int e = g < n_groups ? offsets[g + 1] : 0;
-        e = e < rows ? e : rows;
-        e = e > end ? e : end;
-        e = wave_scan_max(e);
-        int s = __shfl_up(e, 1, 64);
-        s = lane ? s : end;
-        const int n = (e - s + unit - 1) / unit;
-        const int p = wave_scan_add(n);
-        const uint64_t hit = __builtin_amdgcn_ballot_w64(units + p > u);
+        const MxSpan x = mx_span(offsets, n_groups, rows, unit, base, end);
+        const uint64_t hit = __builtin_amdgcn_ballot_w64(units + x.p > u);
         if (hit) {
             const int at = __builtin_ctzll(hit);
-            const int gs = lane_value(s, at), ge = lane_value(e, at);
+            const int gs = lane_value(x.s, at), ge = lane_value(x.e, at);
             out.group = base + at;
-            out.first = units + lane_value(p - n, at);
+            out.first = units + lane_value(x.p - x.n, at);
             out.group_row0 = gs;
             out.group_rows = ge - gs;
             out.row0 = gs + (u - out.first) * unit;
             out.rows = ge - out.row0 < unit ? ge - out.row0 : unit;
-            return true;
+            return;
         }
-        end = lane_value(e, 63);
-        units += lane_value(p, 63);
+        end = lane_value(x.e, 63);
+        units += lane_value(x.p, 63);
     }
     out.group = n_groups;
     out.first = units;
     out.group_row0 = end;
     out.group_rows = rows - end;
     out.row0 = end + (u - units) * unit;
-    if (out.row0 >= rows) return false;
     out.rows = rows - out.row0 < unit ? rows - out.row0 : unit;
-    return true;
 }
 
 // All units of the groups and of the rows in none.  All 64 lanes call.
 __device__ __forceinline__ int64_t mx_units(const int32_t* offsets, int n_groups, int rows, int unit) {
-    const int lane = threadIdx.x & 63;
     int end = 0;
     int64_t units = 0;
     for (int base = 0; base < n_groups; base += 64) {
-        const int g = base + lane;
-        int e = g < n_groups ? offsets[g + 1] : 0;
-        e = e < rows ? e : rows;
-        e = e > end ? e : end;
-        e = wave_scan_max(e);
-        int s = __shfl_up(e, 1, 64);
-        s = lane ? s : end;
-        units += lane_value(wave_scan_add((e - s + unit - 1) / unit), 63);
-        end = lane_value(e, 63);
+        const MxSpan x = mx_span(offsets, n_groups, rows, unit, base, end);
+        units += lane_value(x.p, 63);
+        end = lane_value(x.e, 63);
     }
     return units + (rows - end + unit - 1) / unit;
 }
@@ -135,29 +134,20 @@ __device__ __forceinline__ int64_t mx_units(const int32_t* offsets, int n_groups
 // Group g's rows and the number of `unit`-row units before it.  All 64 lanes call.
 __device__ __forceinline__ void mx_group(const int32_t* offsets, int n_groups, int rows, int unit, int g,
                                          MxUnit& out) {
-    const int lane = threadIdx.x & 63;
     int end = 0;
     int64_t units = 0;
-    for (int base = 0; base < n_groups; base += 64) {
-        const int q = base + lane;
-        int e = q < n_groups ? offsets[q + 1] : 0;
-        e = e < rows ? e : rows;
-        e = e > end ? e : end;
-        e = wave_scan_max(e);
-        int s = __shfl_up(e, 1, 64);
-        s = lane ? s : end;
-        const int n = (e - s + unit - 1) / unit;
-        const int p = wave_scan_add(n);
+    for (int base = 0;; base += 64) {
+        const MxSpan x = mx_span(offsets, n_groups, rows, unit, base, end);
         if (g < base + 64) {
             const int at = g - base;
             out.group = g;
-            out.first = units + lane_value(p - n, at);
-            out.group_row0 = out.row0 = lane_value(s, at);
-            out.group_rows = out.rows = lane_value(e, at) - out.row0;
+            out.first = units + lane_value(x.p - x.n, at);
+            out.group_row0 = out.row0 = lane_value(x.s, at);
+            out.group_rows = out.rows = lane_value(x.e, at) - out.row0;
             return;
         }
-        end = lane_value(e, 63);
-        units += lane_value(p, 63);
+        end = lane_value(x.e, 63);
+        units += lane_value(x.p, 63);
     }
 }
 
@@ -172,6 +162,36 @@ __device__ __forceinline__ void mx_tile_of(unsigned bid, unsigned tiles_m, unsig
     const unsigned rows = tiles_m - first < 8 ? tiles_m - first : 8, in = id - group * 8 * tiles_n;
     tm = first + in % rows;
     tn = in / rows;
+}
+
+// The tile of workgroup `bid` when the rows are grouped: tiles_n columns of units.  False past
+// the last unit (grids are sized for the worst offsets).  With up to 64 groups the offsets are
+// read and scanned once.
+__device__ __forceinline__ bool mx_find_tile(const int32_t* offsets, int n_groups, int rows, int unit,
+                                             unsigned bid, unsigned tiles_n, unsigned& tm, unsigned& tn,
+                                             MxUnit& out) {
+    if (n_groups > 64) {
+        const unsigned units = (unsigned)mx_units(offsets, n_groups, rows, unit);
+        if (bid >= units * tiles_n) return false;
+        mx_tile_of(bid, units, tiles_n, tm, tn);
+        mx_find_unit(offsets, n_groups, rows, unit, tm, out);
+        return true;
+    }
+    const MxSpan x = mx_span(offsets, n_groups, rows, unit, 0, 0);
+    const int grouped = lane_value(x.p, 63), end = lane_value(x.e, 63);
+    const unsigned units = (unsigned)(grouped + (rows - end + unit - 1) / unit);
+    if (bid >= units * tiles_n) return false;
+    mx_tile_of(bid, units, tiles_n, tm, tn);
+    const bool in = tm < (unsigned)grouped;
+    const int at = in ? (int)__builtin_ctzll(__builtin_amdgcn_ballot_w64(x.p > (int)tm)) : 0;
+    const int gs = in ? lane_value(x.s, at) : end, ge = in ? lane_value(x.e, at) : rows;
+    out.group = in ? at : n_groups;
+    out.first = in ? lane_value(x.p - x.n, at) : grouped;
+    out.group_row0 = gs;
+    out.group_rows = ge - gs;
+    out.row0 = gs + (tm - out.first) * unit;
+    out.rows = ge - out.row0 < unit ? ge - out.row0 : unit;
+    return true;
 }
 
 // ---------------------------------------------------------------- host checks

@@ -86,11 +86,8 @@ __global__ __launch_bounds__(256, 1) void k_mx_tiles(MxGArgs g, unsigned tiles_n
     const uint8_t *bc = g.bc, *bs = g.bs;
     T* c = (T*)g.c;
     if constexpr (MODE == MxRows) {
-        const unsigned units = (unsigned)mx_units(g.offsets, g.n_groups, (int)g.M, Tile::BM);
-        if (blockIdx.x >= units * tiles_n) return;
-        mx_tile_of(blockIdx.x, units, tiles_n, tm, tn);
         MxUnit u;
-        mx_find_unit(g.offsets, g.n_groups, (int)g.M, Tile::BM, tm, u);
+        if (!mx_find_tile(g.offsets, g.n_groups, (int)g.M, Tile::BM, blockIdx.x, tiles_n, tm, tn, u)) return;
         m0 = u.row0, m1 = u.row0 + u.rows;
         if (u.group == g.n_groups) nst = 0;
         else bc += u.group * g.N * pitch, bs += u.group * g.N * spitch;

@@ -116,17 +116,10 @@ __device__ __forceinline__ uint32_t codes_of(const Oct<T>& o, uint32_t code, boo
     return code == 255u ? 0u : w;
 }
 
-// DPP moves within quads and within rows of 16 lanes.
-template <int CTRL>
-__device__ __forceinline__ uint32_t dpp(uint32_t v) {
-    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
-}
-constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kRor4 = 0x124, kRor8 = 0x128;
-
 // Largest over the four lanes of a quad, which hold one block.
 __device__ __forceinline__ uint32_t quad_max(uint32_t m) {
-    m = max(m, dpp<kXor1>(m));
-    return max(m, dpp<kXor2>(m));
+    m = max(m, (uint32_t)dpp<kXor1>(0, (int)m));
+    return max(m, (uint32_t)dpp<kXor2>(0, (int)m));
 }
 
 // Rowwise copy alone: a lane per eight elements, a quad per block, so that loads and stores
@@ -176,11 +169,8 @@ __global__ __launch_bounds__(256) void k_mx_tile(MxQArgs g, unsigned units, unsi
     int64_t b = 0, row0, rows, kp0;
     bool has_col = g.cc != nullptr;
     if (g.n_groups) {
-        const unsigned n = (unsigned)mx_units(g.offsets, g.n_groups, (int)g.rows, kMxPad);
-        if (blockIdx.x >= n * col_tiles) return;
-        mx_tile_of(blockIdx.x, n, col_tiles, u, ct);
         MxUnit m;
-        mx_find_unit(g.offsets, g.n_groups, (int)g.rows, kMxPad, u, m);
+        if (!mx_find_tile(g.offsets, g.n_groups, (int)g.rows, kMxPad, blockIdx.x, col_tiles, u, ct, m)) return;
         row0 = m.row0, rows = m.rows, kp0 = (int64_t)u * kMxPad;
         if (m.group == g.n_groups) has_col = false;
     } else {
@@ -217,8 +207,8 @@ __global__ __launch_bounds__(256) void k_mx_tile(MxQArgs g, unsigned units, unsi
             // the scale bytes of the four blocks in 16 lanes: of one bfloat16 row, or of two
             // float32 rows, in one store a row
             uint32_t sc = code << (8 * ((t >> 2) & 3));
-            sc |= dpp<kRor4>(sc);
-            sc |= dpp<kRor8>(sc);
+            sc |= (uint32_t)dpp<kRor4>(0, (int)sc);
+            sc |= (uint32_t)dpp<kRor8>(0, (int)sc);
             if (r < rows) {
                 *(uint32_t*)(g.rc + e / 2) = w;
                 if (tc == 0) {
@@ -266,8 +256,8 @@ __global__ __launch_bounds__(256) void k_mx_tile(MxQArgs g, unsigned units, unsi
             w[k] = codes_of<SR>(v, code, g.sr_col, e + 8 * k, 1, g);
         }
         uint32_t sc = code << (8 * rb);
-        sc |= dpp<kXor1>(sc);
-        sc |= dpp<kXor2>(sc);
+        sc |= (uint32_t)dpp<kXor1>(0, (int)sc);
+        sc |= (uint32_t)dpp<kXor2>(0, (int)sc);
         if (c < g.cols) {
             *(uint4*)(g.cc + e / 2) = make_uint4(w[0], w[1], w[2], w[3]);
             if (rb == 0) *(uint32_t*)(g.cs + e / 32) = sc;
@@ -331,17 +321,17 @@ __global__ __launch_bounds__(256) void k_mx_decode(MxDArgs g) {
 // rows, 16 lanes per row.
 constexpr int kDecodeSteps = 4;
 template <typename T>
-__global__ __launch_bounds__(256) void k_mx_decode_grouped(MxDArgs g, unsigned units) {
-    const int64_t u = blockIdx.x % units;
+__global__ __launch_bounds__(256) void k_mx_decode_grouped(MxDArgs g, unsigned row_tiles) {
+    unsigned u, rt;
     MxUnit m;
-    if (!mx_find_unit(g.offsets, g.n_groups, (int)g.k, kMxPad, u, m)) return;
+    if (!mx_find_tile(g.offsets, g.n_groups, (int)g.k, kMxPad, blockIdx.x, row_tiles, u, rt, m)) return;
     const bool in = m.group != g.n_groups;
-    const int64_t row0 = (int64_t)(blockIdx.x / units) * (16 * kDecodeSteps) + (threadIdx.x >> 4);
+    const int64_t row0 = (int64_t)rt * (16 * kDecodeSteps) + (threadIdx.x >> 4);
     const int j = (int)(threadIdx.x & 15) * 8;
     uint32_t w[kDecodeSteps], code[kDecodeSteps];
 #pragma unroll
     for (int i = 0; i < kDecodeSteps; ++i) {
-        const int64_t r = row0 + 16 * i, e = r * g.kp + u * kMxPad + j;
+        const int64_t r = row0 + 16 * i, e = r * g.kp + (int64_t)u * kMxPad + j;
         const bool ok = in && r < g.n;
         w[i] = ok ? *(const uint32_t*)(g.codes + e / 2) : 0u;
         code[i] = ok ? g.scales[e / 32] : 0u;
@@ -436,10 +426,10 @@ extern "C" int mxfp4_dequantize(const mxfp4_tensor* q, int64_t n, int64_t k, con
     const hipStream_t st = (hipStream_t)stream;
     if (n_groups) {
         // one unit more than the copy holds: the rows in no group
-        const unsigned units = (unsigned)(g.kp / kMxPad + 1);
-        const dim3 grid((unsigned)((n + 16 * kDecodeSteps - 1) / (16 * kDecodeSteps) * units));
-        if (out_dtype == NVFP4_BF16) k_mx_decode_grouped<uint16_t><<<grid, 256, 0, st>>>(g, units);
-        else k_mx_decode_grouped<float><<<grid, 256, 0, st>>>(g, units);
+        const unsigned row_tiles = (unsigned)((n + 16 * kDecodeSteps - 1) / (16 * kDecodeSteps));
+        const dim3 grid((unsigned)(g.kp / kMxPad + 1) * row_tiles);
+        if (out_dtype == NVFP4_BF16) k_mx_decode_grouped<uint16_t><<<grid, 256, 0, st>>>(g, row_tiles);
+        else k_mx_decode_grouped<float><<<grid, 256, 0, st>>>(g, row_tiles);
     } else {
         const int64_t octs = n * (g.kp / 8), per = 256 * kRowSteps;
         const dim3 grid((unsigned)((octs + per - 1) / per));
