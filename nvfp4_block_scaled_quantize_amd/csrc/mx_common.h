@@ -3,12 +3,16 @@
 #include "mxfp4.h"
 #include "device_common.h"
 
+#include <atomic>
+
 namespace nvfp4 {
 
 constexpr uint32_t kTagMxSR = 0x4D585352u;
 constexpr int kMxBlock = 32;    // elements per E8M0 scale
 constexpr int kMxPad = 128;     // a copy's K extent is a multiple of this
 constexpr int64_t kMxMaxK = (int64_t)1 << 23;   // 256 rows of codes stay within 2^30 bytes
+
+typedef int int8v __attribute__((ext_vector_type(8)));
 
 inline int64_t mx_pad(int64_t k) { return (k + kMxPad - 1) / kMxPad * kMxPad; }
 
@@ -19,6 +23,7 @@ inline int64_t mx_pad(int64_t k) { return (k + kMxPad - 1) / kMxPad * kMxPad; }
 // both rules' lower bound gives: amax < 2^-126 <= 6 * 2^-127.  `above`: the largest fraction
 // field that does not round up, kMxCeilAbove or kMxFloorAbove.
 constexpr uint32_t kMxCeilAbove = 0x400000u, kMxFloorAbove = 0x7FFFFFu;
+inline uint32_t mx_above(int rule) { return rule == MXFP4_SCALE_CEIL ? kMxCeilAbove : kMxFloorAbove; }
 __device__ __forceinline__ uint32_t mx_scale_code(uint32_t amax_bits, uint32_t above) {
     uint32_t e = amax_bits >> 23;
     if (e == 255u) return 255u;
@@ -32,6 +37,73 @@ __device__ __forceinline__ float mx_scale_value(uint32_t code) {
     return __uint_as_float(b > 0x400000u ? b : 0x400000u);
 }
 
+// ---------------------------------------------------------------- elements
+// Eight consecutive elements of a block.
+template <typename T> struct Oct {};
+template <> struct Oct<uint16_t> { uint32_t w[4]; };
+template <> struct Oct<float> { float v[8]; };
+
+// Loads of any alignment: rows may start at any element, and the hardware splits what
+// straddles.  left: elements up to the row's end (may be <= 0); the rest are zeros.
+template <typename T>
+__device__ __forceinline__ Oct<T> load_oct(const T* p, int64_t left) {
+    Oct<T> o;
+    if (left >= 8) {
+        __builtin_memcpy(&o, p, sizeof(o));
+    } else {
+        T e[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) e[i] = i < left ? p[i] : (T)0;
+        __builtin_memcpy(&o, e, sizeof(o));
+    }
+    return o;
+}
+
+typedef unsigned short ushort2v __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2v __attribute__((ext_vector_type(2)));
+
+// Magnitude bits of two packed bfloat16 each: they order as the values do.
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(ushort2v, a),
+                                                                  __builtin_bit_cast(ushort2v, b)));
+}
+
+// binary32 bits of the largest magnitude
+__device__ __forceinline__ uint32_t max_bits(const Oct<uint16_t>& o) {
+    uint32_t m = o.w[0] & 0x7FFF7FFFu;
+#pragma unroll
+    for (int i = 1; i < 4; ++i) m = max_bf16x2(m, o.w[i] & 0x7FFF7FFFu);
+    return max(m << 16, m & 0xFFFF0000u);
+}
+__device__ __forceinline__ uint32_t max_bits(const Oct<float>& o) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(o.v[i]) & 0x7FFFFFFFu);
+    return m;
+}
+
+__device__ __forceinline__ float value(const Oct<uint16_t>& o, int i) {
+    return __uint_as_float((i & 1) ? o.w[i >> 1] & 0xFFFF0000u : o.w[i >> 1] << 16);
+}
+__device__ __forceinline__ float value(const Oct<float>& o, int i) { return o.v[i]; }
+
+// Nearest even: eight codes of o / cs (cs a power of two).
+__device__ __forceinline__ uint32_t codes_rne(const Oct<uint16_t>& o, float cs) {
+    uint32_t w = 0;
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf16x2v, o.w[0]), cs, 0);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf16x2v, o.w[1]), cs, 1);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf16x2v, o.w[2]), cs, 2);
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf16x2v, o.w[3]), cs, 3);
+}
+__device__ __forceinline__ uint32_t codes_rne(const Oct<float>& o, float cs) {
+    uint32_t w = 0;
+    w = cvt_fp4x2<0>(w, o.v[0], o.v[1], cs);
+    w = cvt_fp4x2<1>(w, o.v[2], o.v[3], cs);
+    w = cvt_fp4x2<2>(w, o.v[4], o.v[5], cs);
+    return cvt_fp4x2<3>(w, o.v[6], o.v[7], cs);
+}
+
+// ---------------------------------------------------------------- groups of rows
 // A unit (`unit` consecutive rows, or fewer at a group's end) of the rows of a grouped matrix.
 struct MxUnit {
     int group;        // n_groups for the rows past the last group
@@ -53,6 +125,12 @@ __device__ __forceinline__ int dpp(int old, int v) {
     return __builtin_amdgcn_update_dpp(old, v, CTRL, ROWS, 0xF, false);
 }
 constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kRor4 = 0x124, kRor8 = 0x128, kWaveShr1 = 0x138;
+
+// Largest over the four lanes of a quad, which hold one block.
+__device__ __forceinline__ uint32_t quad_max(uint32_t m) {
+    m = max(m, (uint32_t)dpp<kXor1>(0, (int)m));
+    return max(m, (uint32_t)dpp<kXor2>(0, (int)m));
+}
 
 // Inclusive scan over the wave's 64 lanes of non-negative values: within rows of 16, then the
 // last lane of rows 0 and 2 into rows 1 and 3, then lane 31 into the upper half.
@@ -193,6 +271,61 @@ __device__ __forceinline__ bool mx_find_tile(const int32_t* offsets, int n_group
     out.rows = ge - out.row0 < unit ? ge - out.row0 : unit;
     return true;
 }
+
+// ---------------------------------------------------------------- products
+// A product.  Groups: rows (A's and C's rows [offsets[g], offsets[g+1]) with B's matrix g) or
+// ragged K (K positions of group g, C's matrix g).
+enum { MxDense = 0, MxRows = 1, MxK = 2 };
+struct MxGArgs {
+    const uint8_t *ac, *as, *bc, *bs;
+    int64_t M, N, kp;           // kp: K extent of both operands' rows (a multiple of 128)
+    int64_t k_rows;             // MxK: rows that the groups divide
+    void* c;
+    int64_t ldc;
+    const int32_t* offsets;
+    int n_groups;
+};
+
+// A product with few rows (mx_few.hip): A packed (x null), or x to quantize rowwise.
+struct MxFArgs {
+    MxGArgs g;
+    const void* x;
+    int64_t ldx, K;
+    uint32_t above;
+};
+// A packed with at most 16 rows, not grouped.
+int mx_few_packed(const MxFArgs& f, int c_dtype, hipStream_t st);
+// x: at most 16 rows, or grouped (in units of 16 rows of a group).
+int mx_few_linear(const MxFArgs& f, int x_dtype, int c_dtype, hipStream_t st);
+// Whether a workgroup's rows of A fit into LDS.
+bool mx_few_fits(int64_t M, int64_t kp);
+
+constexpr int kMxMaxLds = 160 * 1024;
+// Lets a kernel use `bytes` of LDS, once per device (a bit of `ready` each).
+inline int mx_allow_lds(const void* kernel, int bytes, std::atomic<uint64_t>& ready) {
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess) return NVFP4_ERR_HIP;
+    const uint64_t bit = (uint64_t)1 << (dev & 63);
+    if (dev < 64 && (ready.load(std::memory_order_relaxed) & bit)) return NVFP4_OK;
+    if (hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes) != hipSuccess)
+        return NVFP4_ERR_HIP;
+    ready.fetch_or(bit, std::memory_order_relaxed);
+    return NVFP4_OK;
+}
+
+// A grid's threads are counted in 32 bits.
+inline bool mx_grid_fits(int64_t blocks, int threads) { return blocks * threads < ((int64_t)1 << 32); }
+
+typedef float float4v __attribute__((ext_vector_type(4)));
+
+// An operand fragment: the instruction's E2M1 form reads the first four of eight registers.
+__device__ __forceinline__ int8v mx_frag(int4v v) {
+    return __builtin_shufflevector(v, v, 0, 1, 2, 3, -1, -1, -1, -1);
+}
+constexpr int kE2M1 = 4;
+
+__device__ __forceinline__ void store_c(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store_c(uint16_t* p, float v) { *p = __builtin_bit_cast(uint16_t, (__bf16)v); }
 
 // ---------------------------------------------------------------- host checks
 // `used`: the copy has elements, so its arrays must exist.

@@ -22,71 +22,6 @@ struct MxQArgs {
     uint32_t k0, k1;                // Philox key
 };
 
-// Eight consecutive elements of a block.
-template <typename T> struct Oct;
-template <> struct Oct<uint16_t> { uint32_t w[4]; };
-template <> struct Oct<float> { float v[8]; };
-
-// Loads of any alignment: rows may start at any element, and the hardware splits what
-// straddles.  left: elements up to the row's end (may be <= 0); the rest are zeros.
-template <typename T>
-__device__ __forceinline__ Oct<T> load_oct(const T* p, int64_t left) {
-    Oct<T> o;
-    if (left >= 8) {
-        __builtin_memcpy(&o, p, sizeof(o));
-    } else {
-        T e[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) e[i] = i < left ? p[i] : (T)0;
-        __builtin_memcpy(&o, e, sizeof(o));
-    }
-    return o;
-}
-
-typedef unsigned short ushort2v __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x2v __attribute__((ext_vector_type(2)));
-
-// Magnitude bits of two packed bfloat16 each: they order as the values do.
-__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
-    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(ushort2v, a),
-                                                                  __builtin_bit_cast(ushort2v, b)));
-}
-
-// binary32 bits of the largest magnitude
-__device__ __forceinline__ uint32_t max_bits(const Oct<uint16_t>& o) {
-    uint32_t m = o.w[0] & 0x7FFF7FFFu;
-#pragma unroll
-    for (int i = 1; i < 4; ++i) m = max_bf16x2(m, o.w[i] & 0x7FFF7FFFu);
-    return max(m << 16, m & 0xFFFF0000u);
-}
-__device__ __forceinline__ uint32_t max_bits(const Oct<float>& o) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(o.v[i]) & 0x7FFFFFFFu);
-    return m;
-}
-
-__device__ __forceinline__ float value(const Oct<uint16_t>& o, int i) {
-    return __uint_as_float((i & 1) ? o.w[i >> 1] & 0xFFFF0000u : o.w[i >> 1] << 16);
-}
-__device__ __forceinline__ float value(const Oct<float>& o, int i) { return o.v[i]; }
-
-// Nearest even: eight codes of o / cs (cs a power of two).
-__device__ __forceinline__ uint32_t codes_rne(const Oct<uint16_t>& o, float cs) {
-    uint32_t w = 0;
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf16x2v, o.w[0]), cs, 0);
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf16x2v, o.w[1]), cs, 1);
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf16x2v, o.w[2]), cs, 2);
-    return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf16x2v, o.w[3]), cs, 3);
-}
-__device__ __forceinline__ uint32_t codes_rne(const Oct<float>& o, float cs) {
-    uint32_t w = 0;
-    w = cvt_fp4x2<0>(w, o.v[0], o.v[1], cs);
-    w = cvt_fp4x2<1>(w, o.v[2], o.v[3], cs);
-    w = cvt_fp4x2<2>(w, o.v[4], o.v[5], cs);
-    return cvt_fp4x2<3>(w, o.v[6], o.v[7], cs);
-}
-
 // Stochastic: x / s in binary32 (exact but for results below 2^-126, which round to 0 with
 // every draw that f 2^16 < 1 allows), then the conversion at unit scale.  e: the first
 // element's index in the copy (a multiple of 8).
@@ -114,12 +49,6 @@ __device__ __forceinline__ uint32_t codes_of(const Oct<T>& o, uint32_t code, boo
     if (SR && sr) w = codes_sr(o, code, e, copy, g.k0, g.k1);
     else w = codes_rne(o, mx_scale_value(code));
     return code == 255u ? 0u : w;
-}
-
-// Largest over the four lanes of a quad, which hold one block.
-__device__ __forceinline__ uint32_t quad_max(uint32_t m) {
-    m = max(m, (uint32_t)dpp<kXor1>(0, (int)m));
-    return max(m, (uint32_t)dpp<kXor2>(0, (int)m));
 }
 
 // Rowwise copy alone: a lane per eight elements, a quad per block, so that loads and stores
@@ -402,7 +331,7 @@ extern "C" int mxfp4_quantize(const void* x, int dtype, int64_t batch, int64_t r
     if (p->colwise) g.cc = col_out->codes, g.cs = col_out->scales;
     g.k0 = (uint32_t)p->seed, g.k1 = (uint32_t)(p->seed >> 32);
     const hipStream_t st = (hipStream_t)stream;
-    g.above = p->scale_rule == MXFP4_SCALE_CEIL ? kMxCeilAbove : kMxFloorAbove;
+    g.above = mx_above(p->scale_rule);
     g.sr_row = p->round_row == NVFP4_SR, g.sr_col = p->round_col == NVFP4_SR;
     const bool sr = (g.rc && g.sr_row) || (g.cc && g.sr_col);
     if (dtype == NVFP4_BF16) sr ? launch_quantize<uint16_t, true>(g, st) : launch_quantize<uint16_t, false>(g, st);

@@ -95,14 +95,18 @@ def test_scales_far_apart_and_nan(nv):
     check(c[~nan], want[~nan], absdot[~nan], "beside NaN f32")
 
 
-def test_inputs_with_nan_and_inf(nv):
+@pytest.mark.parametrize("M", [7, 14, 40])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_inputs_with_nan_and_inf(nv, M, dtype):
     """A token with a NaN or an infinity gives NaN in its own row of Y only."""
-    x = torch.randn(40, 300, device=dev())
-    x[3, 200], x[9, 0] = float("nan"), float("inf")
+    x = torch.randn(M, 300, device=dev()).to(dtype)
+    x[3, 200], x[6, 0] = float("nan"), float("inf")
     w = nv.mxfp4_quantize(torch.randn(50, 300, device=dev()), nv.mxfp4_quant_params())[0]
-    y = nv.mxfp4_linear(x, w)
-    rows = torch.isnan(y).any(1).nonzero().flatten().tolist()
-    assert rows == [3, 9] and torch.isnan(y[rows]).all() and torch.isfinite(y[[0, 10, 39]]).all()
+    off = torch.tensor([0, 5, M], dtype=torch.int32, device=dev())
+    stack = nv.MXTensor(torch.stack([w.codes] * 2), torch.stack([w.scales] * 2), 300)
+    for y in (nv.mxfp4_linear(x, w), nv.mxfp4_linear(x, stack, offsets=off)):
+        assert torch.isnan(y).any(1).nonzero().flatten().tolist() == [3, 6]
+        assert torch.isnan(y[[3, 6]]).all()
 
 
 def spread_offsets(rows, groups, seed, tail=0):
