@@ -326,6 +326,11 @@ constexpr int kE2M1 = 4;
 
 __device__ __forceinline__ void store_c(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_c(uint16_t* p, float v) { *p = __builtin_bit_cast(uint16_t, (__bf16)v); }
+// bfloat16 past the caches
+__device__ __forceinline__ void stream_c(float* p, float v) { *p = v; }
+__device__ __forceinline__ void stream_c(uint16_t* p, float v) {
+    __builtin_nontemporal_store(__builtin_bit_cast(uint16_t, (__bf16)v), p);
+}
 
 // ---------------------------------------------------------------- host checks
 // `used`: the copy has elements, so its arrays must exist.

@@ -203,30 +203,46 @@ struct MxDArgs {
     int64_t ld;
 };
 
-// Eight decoded elements, of which the first `left` are stored (any alignment).  bfloat16: exact
-// for copies of bfloat16 values, nearest even otherwise.
+// The decode's piece of a lane: 16 bytes of output, so that a wave's stores are contiguous.
+template <typename T> struct Piece;
+template <> struct Piece<uint16_t> { static constexpr int n = 8; using Codes = uint32_t; };
+template <> struct Piece<float> { static constexpr int n = 4; using Codes = uint16_t; };
+
+// Decoded elements, of which the first `left` are stored (any alignment).  bfloat16: exact for
+// copies of bfloat16 values, nearest even otherwise.  The stores stream past the caches: 8192 x
+// 9216 bfloat16 28 us against 38 with ordinary ones, and 60 against 66 together with a
+// quantizer that reads them back.
 template <typename T>
-__device__ __forceinline__ void decode_oct(uint32_t w, uint32_t code, T* p, int64_t left) {
+__device__ __forceinline__ void decode_piece(uint32_t w, uint32_t code, T* p, int64_t left) {
+    constexpr int n = Piece<T>::n;
     const float s = code == 255u ? __builtin_nanf("") : mx_scale_value(code);
     const float2v v[4] = {fp4x2_to_f32<0>(w), fp4x2_to_f32<1>(w), fp4x2_to_f32<2>(w), fp4x2_to_f32<3>(w)};
-    T e[8];
+    T e[n];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < n; ++i) {
         const float f = v[i >> 1][i & 1] * s;
         if constexpr (sizeof(T) == 2) e[i] = __builtin_bit_cast(uint16_t, (__bf16)f);
         else e[i] = f;
     }
-    if (left >= 8) __builtin_memcpy(p, e, sizeof(e));
-    else
+    if (left >= n) {
+        if (((uintptr_t)p & 15) == 0) {
+            int4v q;
+            __builtin_memcpy(&q, e, sizeof(q));
+            __builtin_nontemporal_store(q, (int4v*)p);
+        } else {
+            __builtin_memcpy(p, e, sizeof(e));
+        }
+    } else
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < n; ++i)
             if (i < left) p[i] = e[i];
 }
 
-// Plain copy: a lane per eight elements, as k_mx_rows.
+// Plain copy: consecutive pieces of the padded copy, as k_mx_rows.
 template <typename T>
 __global__ __launch_bounds__(256) void k_mx_decode(MxDArgs g) {
-    const uint32_t per = (uint32_t)(g.kp / 8);
+    constexpr int n = Piece<T>::n;
+    const uint32_t per = (uint32_t)(g.kp / n);
     const int64_t first = (int64_t)blockIdx.x * (256 * kRowSteps), total = g.n * per;
     const int64_t row0 = first / per;
     const uint32_t rem = (uint32_t)(first - row0 * per);
@@ -234,41 +250,55 @@ __global__ __launch_bounds__(256) void k_mx_decode(MxDArgs g) {
 #pragma unroll
     for (int i = 0; i < kRowSteps; ++i) {
         const int64_t at = first + threadIdx.x + 256 * i;
-        w[i] = at < total ? ((const uint32_t*)g.codes)[at] : 0u;
-        code[i] = at < total ? g.scales[at >> 2] : 0u;
+        w[i] = at < total ? ((const typename Piece<T>::Codes*)g.codes)[at] : 0u;
+        code[i] = at < total ? g.scales[at / (32 / n)] : 0u;
     }
 #pragma unroll
     for (int i = 0; i < kRowSteps; ++i) {
         const uint32_t at = rem + threadIdx.x + 256 * i, dr = at / per;
-        const int64_t r = row0 + dr, k = (int64_t)(at - dr * per) * 8;
+        const int64_t r = row0 + dr, k = (int64_t)(at - dr * per) * n;
         if (first + threadIdx.x + 256 * i < total)
-            decode_oct(w[i], code[i], (T*)g.out + r * g.ld + k, g.k - k);
+            decode_piece(w[i], code[i], (T*)g.out + r * g.ld + k, g.k - k);
     }
 }
 
-// Grouped columnwise copy: a workgroup takes a 128-row unit's positions of 64 of the copy's
-// rows, 16 lanes per row.
+// Grouped columnwise copy: a workgroup takes a 128-row unit's positions of some of the copy's
+// rows.
 constexpr int kDecodeSteps = 4;
+template <typename T> constexpr int kDecodeRows = 256 * Piece<T>::n / kMxPad * kDecodeSteps;
 template <typename T>
 __global__ __launch_bounds__(256) void k_mx_decode_grouped(MxDArgs g, unsigned row_tiles) {
+    constexpr int n = Piece<T>::n, kLanes = kMxPad / n, kRows = 256 / kLanes;
     unsigned u, rt;
     MxUnit m;
     if (!mx_find_tile(g.offsets, g.n_groups, (int)g.k, kMxPad, blockIdx.x, row_tiles, u, rt, m)) return;
     const bool in = m.group != g.n_groups;
-    const int64_t row0 = (int64_t)rt * (16 * kDecodeSteps) + (threadIdx.x >> 4);
-    const int j = (int)(threadIdx.x & 15) * 8;
+    const int64_t row0 = (int64_t)rt * kDecodeRows<T> + threadIdx.x / kLanes;
+    const int j = (int)(threadIdx.x % kLanes) * n;
     uint32_t w[kDecodeSteps], code[kDecodeSteps];
 #pragma unroll
     for (int i = 0; i < kDecodeSteps; ++i) {
-        const int64_t r = row0 + 16 * i, e = r * g.kp + (int64_t)u * kMxPad + j;
+        const int64_t r = row0 + kRows * i, e = r * g.kp + (int64_t)u * kMxPad + j;
         const bool ok = in && r < g.n;
-        w[i] = ok ? *(const uint32_t*)(g.codes + e / 2) : 0u;
+        w[i] = ok ? *(const typename Piece<T>::Codes*)(g.codes + e / 2) : 0u;
         code[i] = ok ? g.scales[e / 32] : 0u;
     }
 #pragma unroll
     for (int i = 0; i < kDecodeSteps; ++i) {
-        const int64_t r = row0 + 16 * i;
-        if (r < g.n) decode_oct(w[i], code[i], (T*)g.out + r * g.ld + m.row0 + j, m.rows - j);
+        const int64_t r = row0 + kRows * i;
+        if (r < g.n) decode_piece(w[i], code[i], (T*)g.out + r * g.ld + m.row0 + j, m.rows - j);
+    }
+}
+
+template <typename T>
+static void launch_decode(const MxDArgs& g, hipStream_t st) {
+    if (g.n_groups) {
+        // one unit more than the copy holds: the rows in no group
+        const unsigned row_tiles = (unsigned)((g.n + kDecodeRows<T> - 1) / kDecodeRows<T>);
+        k_mx_decode_grouped<T><<<dim3((unsigned)(g.kp / kMxPad + 1) * row_tiles), 256, 0, st>>>(g, row_tiles);
+    } else {
+        const int64_t pieces = g.n * (g.kp / Piece<T>::n), per = 256 * kRowSteps;
+        k_mx_decode<T><<<dim3((unsigned)((pieces + per - 1) / per)), 256, 0, st>>>(g);
     }
 }
 
@@ -353,17 +383,7 @@ extern "C" int mxfp4_dequantize(const mxfp4_tensor* q, int64_t n, int64_t k, con
     MxDArgs g = {q->codes, q->scales, n, k, n_groups ? mxfp4_grouped_k(k, n_groups) : mx_pad(k),
                  offsets, (int)n_groups, out, ld_out};
     const hipStream_t st = (hipStream_t)stream;
-    if (n_groups) {
-        // one unit more than the copy holds: the rows in no group
-        const unsigned row_tiles = (unsigned)((n + 16 * kDecodeSteps - 1) / (16 * kDecodeSteps));
-        const dim3 grid((unsigned)(g.kp / kMxPad + 1) * row_tiles);
-        if (out_dtype == NVFP4_BF16) k_mx_decode_grouped<uint16_t><<<grid, 256, 0, st>>>(g, row_tiles);
-        else k_mx_decode_grouped<float><<<grid, 256, 0, st>>>(g, row_tiles);
-    } else {
-        const int64_t octs = n * (g.kp / 8), per = 256 * kRowSteps;
-        const dim3 grid((unsigned)((octs + per - 1) / per));
-        if (out_dtype == NVFP4_BF16) k_mx_decode<uint16_t><<<grid, 256, 0, st>>>(g);
-        else k_mx_decode<float><<<grid, 256, 0, st>>>(g);
-    }
+    if (out_dtype == NVFP4_BF16) launch_decode<uint16_t>(g, st);
+    else launch_decode<float>(g, st);
     return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
 }
