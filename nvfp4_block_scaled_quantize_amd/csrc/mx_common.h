@@ -39,17 +39,25 @@ __device__ __forceinline__ float mx_scale_value(uint32_t code) {
 
 // ---------------------------------------------------------------- elements
 // Eight consecutive elements of a block.
+typedef int int4_by2 __attribute__((ext_vector_type(4), aligned(2)));
+typedef int int4_by4 __attribute__((ext_vector_type(4), aligned(4)));
 template <typename T> struct Oct {};
-template <> struct Oct<uint16_t> { uint32_t w[4]; };
-template <> struct Oct<float> { float v[8]; };
+template <> struct Oct<uint16_t> { uint32_t w[4]; using Vec = int4_by2; };
+template <> struct Oct<float> { float v[8]; using Vec = int4_by4; };
 
 // Loads of any alignment: rows may start at any element, and the hardware splits what
-// straddles.  left: elements up to the row's end (may be <= 0); the rest are zeros.
-template <typename T>
+// straddles.  left: elements up to the row's end (may be <= 0); the rest are zeros.  STREAM:
+// past the caches.
+template <typename T, bool STREAM = false>
 __device__ __forceinline__ Oct<T> load_oct(const T* p, int64_t left) {
+    using Vec = typename Oct<T>::Vec;
     Oct<T> o;
     if (left >= 8) {
-        __builtin_memcpy(&o, p, sizeof(o));
+        int4v v[sizeof(o) / 16];
+#pragma unroll
+        for (unsigned i = 0; i < sizeof(o) / 16; ++i)
+            v[i] = STREAM ? __builtin_nontemporal_load((const Vec*)p + i) : ((const Vec*)p)[i];
+        __builtin_memcpy(&o, v, sizeof(o));
     } else {
         T e[8];
 #pragma unroll

@@ -72,11 +72,11 @@ __global__ __launch_bounds__(64 * WAVES) void k_mx_few(MxFArgs f, unsigned tiles
     // The first of x is asked for before W: loads return in order, and x has to be quantized
     // while W is on its way.  A lane takes eight elements, a quad a block.
     const int per = (int)(g.kp / 8), octs = steps ? rows * per : 0;
-    const auto load_x = [&](int i) {
+    const auto load_x = [&](int i) -> Oct<XT> {
         const int r = i / per, k = (i - r * per) * 8;
-        return load_oct((const XT*)f.x + (m0 + r) * f.ldx + k, i < octs ? f.K - k : 0);
+        if constexpr (sizeof(XT) > 1) return load_oct((const XT*)f.x + (m0 + r) * f.ldx + k, i < octs ? f.K - k : 0);
     };
-    Oct<XT> o;
+    [[maybe_unused]] Oct<XT> o;
     if constexpr (sizeof(XT) > 1) o = load_x(t);
     Batch cur = {};
     if (s0 < s1) load(cur, s0);
