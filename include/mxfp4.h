@@ -127,7 +127,8 @@ int mxfp4_gemm_grouped_wgrad(const mxfp4_tensor* a, const mxfp4_tensor* b, const
  * ld_x) quantized rowwise to nearest even by scale_rule, W a copy N x K; or, with offsets,
  * grouped as in mxfp4_gemm_grouped with W holding n_groups matrices.  The result is that of
  * mxfp4_quantize followed by the product.
- *   ws  device workspace of mxfp4_linear_workspace_bytes() bytes, 256-byte aligned */
+ *   ws  device workspace of mxfp4_linear_workspace_bytes() bytes, 256-byte aligned (0 bytes,
+ *       NULL allowed, for the few rows that are quantized inside the product's kernel) */
 size_t mxfp4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t n_groups);
 int mxfp4_linear(const void* x, int dtype, int64_t M, int64_t K, int64_t ld_x, int32_t scale_rule,
                  const mxfp4_tensor* w, int64_t N, const int32_t* offsets, int64_t n_groups,

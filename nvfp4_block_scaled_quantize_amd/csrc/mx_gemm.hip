@@ -311,9 +311,18 @@ static size_t linear_code_bytes(int64_t M, int64_t K) {
     return ((size_t)(M * (mx_pad(K) / 2)) + 255) / 256 * 256;
 }
 
+// Few rows are quantized inside the product, which saves a launch and the workspace, as long as
+// every workgroup's doing so costs less: 8 rows of 6144 x 4096 10.9 against 10.0 us of GPU time
+// with one launch less of host time; 16 rows 16.2 against 10.5.  For groups the same per group:
+// 24 rows over 17 groups 21.5 against 22.1 us, 80 rows 27.5 against 22.6.
+static bool linear_fused(int64_t M, int64_t K, int64_t n_groups) {
+    const int64_t busy = n_groups < M ? n_groups : M;
+    return M > 0 && K > 0 && mx_few_fits(M, mx_pad(K)) && (n_groups ? M <= 2 * busy : M <= 8);
+}
+
 extern "C" size_t mxfp4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t n_groups) {
-    (void)N, (void)n_groups;
-    return M > 0 && K > 0 ? linear_code_bytes(M, K) + (size_t)(M * (mx_pad(K) / 32)) : 0;
+    (void)N;
+    return M > 0 && K > 0 && !linear_fused(M, K, n_groups) ? linear_code_bytes(M, K) + (size_t)(M * (mx_pad(K) / 32)) : 0;
 }
 
 extern "C" int mxfp4_linear(const void* x, int dtype, int64_t M, int64_t K, int64_t ld_x,
@@ -326,16 +335,12 @@ extern "C" int mxfp4_linear(const void* x, int dtype, int64_t M, int64_t K, int6
     if ((uintptr_t)ws & 255) return NVFP4_ERR_ALIGN;
     const mxfp4_tensor q = {(uint8_t*)ws, (uint8_t*)ws + (need ? linear_code_bytes(M, K) : 0)};
     const mxfp4_quant_params p = {1, 0, scale_rule, NVFP4_RNE, NVFP4_RNE, 0};
-    // the product's arguments are checked before the quantization is enqueued
+    // the product's arguments are checked before the quantization is enqueued (without a workspace
+    // there is no packed A to check)
     bool empty;
-    if (int rc = check_gemm(&q, w, M, N, K, c, c_dtype, ldc, &empty)) return rc;
+    if (int rc = check_gemm(need ? &q : w, w, M, N, K, c, c_dtype, ldc, &empty)) return rc;
     if (int rc = mx_check_groups(offsets, n_groups, M)) return rc;
-    // Few rows are quantized inside the product, which saves a launch, as long as every
-    // workgroup's doing so costs less: 8 rows of 6144 x 4096 10.9 against 10.0 us of GPU time
-    // with one launch less of host time; 16 rows 16.2 against 10.5.  For groups the same per
-    // group: 24 rows over 17 groups 21.5 against 22.1 us, 80 rows 27.5 against 22.6.
-    const int64_t busy = n_groups < M ? n_groups : M;
-    if (x && K > 0 && mx_few_fits(M, mx_pad(K)) && (n_groups ? M <= 2 * busy : M <= 8)) {
+    if (x && linear_fused(M, K, n_groups)) {
         if (const int size = mx_dtype_size(dtype); !size) return NVFP4_ERR_DTYPE;
         else if ((uintptr_t)x % size) return NVFP4_ERR_ALIGN;
         if (ld_x < K) return NVFP4_ERR_SHAPE;

@@ -112,8 +112,15 @@ class MXTensor:
         """Uninitialised copy; n: the number of rows, or a tuple (batch, rows)."""
         kp = grouped_k(k, n_groups) if n_groups else padded_k(k)
         n = n if isinstance(n, tuple) else (n,)
-        return MXTensor(torch.empty((*n, kp // 2), dtype=torch.uint8, device=device),
-                        torch.empty((*n, kp // 32), dtype=torch.uint8, device=device), k, n_groups)
+        return MXTensor(_empty(*n, kp // 2, torch.uint8, device), _empty(*n, kp // 32, torch.uint8, device),
+                        k, n_groups)
+
+
+def _empty(*args):
+    """torch.empty(shape, dtype, device) for two or three extents (0.4 us sooner)."""
+    *shape, dtype, device = args
+    strides = (shape[1], 1) if len(shape) == 2 else (shape[1] * shape[2], shape[2], 1)
+    return torch.empty_strided(shape, strides, dtype=dtype, device=device)
 
 
 def padded_k(k):
@@ -190,7 +197,9 @@ def _output(out, shape, dtype, like):
         code = _DTYPES.get(dtype)
         if code is None:
             raise _error(f"unsupported dtype {dtype}")
-        return torch.empty(shape, dtype=dtype, device=like.device), code, shape[-1]
+        if len(shape) > 3:
+            return torch.empty(shape, dtype=dtype, device=like.device), code, shape[-1]
+        return _empty(*shape, dtype, like.device), code, shape[-1]
     device, got, code, pitch = _matrix(out, "out")
     if got != shape or device != like.get_device():
         raise _error(f"out must be a {shape} tensor on the operands' device")
@@ -220,15 +229,23 @@ def mxfp4_quantize(x, params, offsets=None, row_out=None, col_out=None):
     batch = lead[0] if lead else 1
     row = col = rc = cc = None
     if params.rowwise:
-        row = row_out if row_out is not None else MXTensor.empty((*lead, R), C, x.device)
-        rc, got = _operand(row, "row_out", dev)
-        if got[:-1] != (*lead, R) or row.k != C or row.n_groups:
-            raise _error(f"row_out {row.shape} does not hold x {tuple(shape)}")
+        if row_out is None:
+            row = MXTensor.empty((*lead, R), C, x.device)
+            rc = row.c()
+        else:
+            row = row_out
+            rc, got = _operand(row, "row_out", dev)
+            if got[:-1] != (*lead, R) or row.k != C or row.n_groups:
+                raise _error(f"row_out {row.shape} does not hold x {tuple(shape)}")
     if params.colwise:
-        col = col_out if col_out is not None else MXTensor.empty((*lead, C), R, x.device, groups)
-        cc, got = _operand(col, "col_out", dev)
-        if got[:-1] != (*lead, C) or col.k != R or col.n_groups != groups:
-            raise _error(f"col_out {col.shape} does not hold x {tuple(shape)} transposed")
+        if col_out is None:
+            col = MXTensor.empty((*lead, C), R, x.device, groups)
+            cc = col.c()
+        else:
+            col = col_out
+            cc, got = _operand(col, "col_out", dev)
+            if got[:-1] != (*lead, C) or col.k != R or col.n_groups != groups:
+                raise _error(f"col_out {col.shape} does not hold x {tuple(shape)} transposed")
     _check(_lib().mxfp4_quantize(x.data_ptr(), dtype, batch, R, C, pitch,
                                  x.stride(0) if batch > 1 else 0, op, groups, params, rc, cc,
                                  _stream(dev)))
@@ -331,7 +348,7 @@ def mxfp4_linear(x, w, offsets=None, scale_rule=MXFP4_SCALE_FLOOR, out=None, out
     lib = _lib()
     if workspace is None:
         need = lib.mxfp4_linear_workspace_bytes(M, N, K, groups)
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
+        workspace = _empty(1, need, torch.uint8, x.device) if need else None
     elif workspace.get_device() != dev or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise _error("workspace must be a contiguous uint8 tensor on x's device")
     ws, ws_bytes = (workspace.data_ptr(), workspace.numel()) if workspace is not None else (None, 0)

@@ -310,7 +310,7 @@ def test_refusals(nv):
            lambda: nv.mxfp4_linear(x, e(8, 63)), lambda: nv.mxfp4_linear(x, e((1, 8), 64)),
            lambda: nv.mxfp4_linear(x, e((2, 8), 64), offsets=off), lambda: nv.mxfp4_linear(x.half(), e(8, 64)),
            lambda: nv.mxfp4_linear(x, e(8, 64), scale_rule=2),
-           lambda: nv.mxfp4_linear(x.t(), e(8, 8)), lambda: nv.mxfp4_linear(x, e(8, 64), workspace=torch.empty(1, dtype=torch.uint8, device=d)),
+           lambda: nv.mxfp4_linear(x.t(), e(8, 8)), lambda: nv.mxfp4_linear(x.repeat(9, 1), e(8, 64), workspace=torch.empty(1, dtype=torch.uint8, device=d)),
            lambda: nv.mxfp4_gemm(nv.MXTensor(e(8, 64).codes[:, ::2], e(8, 64).scales, 64), e(8, 64)),
            lambda: nv.mxfp4_gemm(nv.MXTensor(e(8, 64).codes.cpu(), e(8, 64).scales, 64), e(8, 64))]
     for i, f in enumerate(bad):
