@@ -334,10 +334,32 @@ constexpr int kE2M1 = 4;
 
 __device__ __forceinline__ void store_c(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_c(uint16_t* p, float v) { *p = __builtin_bit_cast(uint16_t, (__bf16)v); }
-// bfloat16 past the caches
-__device__ __forceinline__ void stream_c(float* p, float v) { *p = v; }
-__device__ __forceinline__ void stream_c(uint16_t* p, float v) {
-    __builtin_nontemporal_store(__builtin_bit_cast(uint16_t, (__bf16)v), p);
+// Four consecutive elements of C into LDS.
+__device__ __forceinline__ void put_c4(float* p, float a, float b, float c, float d) {
+    *(float4v*)p = float4v{a, b, c, d};
+}
+__device__ __forceinline__ void put_c4(uint16_t* p, float a, float b, float c, float d) {
+    typedef __bf16 bf16x4v __attribute__((ext_vector_type(4)));
+    *(bf16x4v*)p = bf16x4v{(__bf16)a, (__bf16)b, (__bf16)c, (__bf16)d};
+}
+// 16 bytes of a row of C, of which `left` elements exist; bfloat16 past the caches.
+__device__ __forceinline__ void stream_c(float* p, int4v v, int64_t left) {
+    if (left >= 4) {
+        *(int4_by4*)p = v;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+            if (i < left) p[i] = __int_as_float(v[i]);
+    }
+}
+__device__ __forceinline__ void stream_c(uint16_t* p, int4v v, int64_t left) {
+    if (left >= 8) {
+        __builtin_nontemporal_store((int4_by2)v, (int4_by2*)p);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 7; ++i)
+            if (i < left) p[i] = (uint16_t)((uint32_t)v[i >> 1] >> (16 * (i & 1)));
+    }
 }
 
 // ---------------------------------------------------------------- host checks

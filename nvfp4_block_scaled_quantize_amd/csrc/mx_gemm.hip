@@ -160,7 +160,7 @@ __global__ __launch_bounds__(256, 1) void k_mx_tiles(MxGArgs g, unsigned tiles_n
             static_for<0, TM * TN>([&](auto mc) {
                 constexpr int m = decltype(mc)::value, i = m / TN, j = m % TN;
                 acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                    mx_frag(a0[i]), mx_frag(b0[j]), acc[i][j], kE2M1, kE2M1, 0, sa[i], 0, sb[j]);
+                    mx_frag(b0[j]), mx_frag(a0[i]), acc[i][j], kE2M1, kE2M1, 0, sb[j], 0, sa[i]);
                 if constexpr (m < TN) b1[m] = frag(s, true, m, 1);
                 else if constexpr (m < TM + TN) a1[m - TN] = frag(s, false, m - TN, 1);
                 __builtin_amdgcn_sched_barrier(0);
@@ -172,7 +172,7 @@ __global__ __launch_bounds__(256, 1) void k_mx_tiles(MxGArgs g, unsigned tiles_n
             static_for<0, TM * TN>([&](auto mc) {
                 constexpr int m = decltype(mc)::value, i = m / TN, j = m % TN;
                 acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                    mx_frag(a1[i]), mx_frag(b1[j]), acc[i][j], kE2M1, kE2M1, 1, sa[i], 1, sb[j]);
+                    mx_frag(b1[j]), mx_frag(a1[i]), acc[i][j], kE2M1, kE2M1, 1, sb[j], 1, sa[i]);
                 constexpr int every = TM * TN / Tile::kLoads;
                 if constexpr (m % every == every - 1) load_codes(s + 3, std::integral_constant<int, m / every>{});
                 if constexpr (m < TN) b0[m] = frag(s + 1, true, m, 0), nb[m] = scale(s + 1, true, m);
@@ -201,21 +201,35 @@ __global__ __launch_bounds__(256, 1) void k_mx_tiles(MxGArgs g, unsigned tiles_n
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no load may write LDS after the wave's end
     }
 
+    // Epilogue.  Register r of lane l is column 8 (r / 4) + 4 (l / 32) + r % 4, row l % 32 of its
+    // 32 x 32: a wave puts 32 rows of its part of C into LDS (its own piece, behind the barrier
+    // that ends the stages' use of it) and stores them from there 16 bytes a lane, a row's 128 or
+    // 64 columns contiguous.
     // bfloat16 stores stream past the caches (grouped 16384 x 4096 x 2048: 122 us against 132 with
     // ordinary ones, and no slower where a quantizer reads C back: 8192 x 9216 x 4096 220 us
     // either way); float32 ones do not (78 against 88 us with such a reader).
-    // register r of lane l is row 8 (r / 4) + 4 (l / 32) + r % 4, column l % 32 of its 32 x 32
-    const int64_t row0 = m0 + wm * (Tile::BM / 2) + 4 * h, col0 = n0 + wn * (Tile::BN / 2) + li;
+    asm volatile("s_barrier" ::: "memory");
+    constexpr int kCols = TN * 32, kRowBytes = kCols * (int)sizeof(T) + 16;
+    constexpr int kPer = 16 / (int)sizeof(T), kLanes = kCols / kPer, kRowsAtOnce = 64 / kLanes;
+    static_assert(4 * 32 * kRowBytes <= Tile::kLds, "the epilogue's rows fit");
+    uint8_t* piece = lds + wid * (32 * kRowBytes);
+    const int64_t col = n0 + wn * (Tile::BN / 2) + (lane % kLanes) * kPer;
 #pragma unroll
-    for (int i = 0; i < TM; ++i)
+    for (int i = 0; i < TM; ++i) {
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            const int64_t row = row0 + i * 32 + 8 * (r >> 2) + (r & 3);
-            if (row < m1)
+        for (int j = 0; j < TN; ++j)
 #pragma unroll
-                for (int j = 0; j < TN; ++j)
-                    if (col0 + j * 32 < g.N) stream_c(c + row * g.ldc + col0 + j * 32, acc[i][j][r]);
+            for (int r = 0; r < 16; r += 4)
+                put_c4((T*)(piece + li * kRowBytes) + j * 32 + 2 * r + 4 * h, acc[i][j][r], acc[i][j][r + 1],
+                       acc[i][j][r + 2], acc[i][j][r + 3]);
+        const int64_t row0 = m0 + wm * (Tile::BM / 2) + i * 32 + lane / kLanes;
+#pragma unroll
+        for (int k = 0; k < 32 / kRowsAtOnce; ++k) {
+            const int4v v = *(const int4v*)(piece + (k * kRowsAtOnce + lane / kLanes) * kRowBytes + (lane % kLanes) * 16);
+            const int64_t row = row0 + k * kRowsAtOnce;
+            if (row < m1) stream_c(c + row * g.ldc + col, v, g.N - col);
         }
+    }
 }
 
 template <typename T, int MODE, int TM, int TN>
