@@ -27,8 +27,6 @@ namespace nvfp4 {
 // a second set of registers; the one barrier of a stage stands between its halves, and the
 // loads for three stages ahead are issued right after it.
 constexpr int kMxStage = 128, kMxStages = 4;
-constexpr int kMxScaleRows = 256;                       // rows of a scale buffer
-constexpr int kMxScaleBytes = kMxScaleRows * 16;
 
 template <int TM, int TN>
 struct MxTile {
@@ -37,7 +35,12 @@ struct MxTile {
     static constexpr int kLoadsA = BM / 64, kLoadsB = BN / 64;   // per wave and stage
     static constexpr int kLoads = kLoadsA + kLoadsB;
     static constexpr int kScales = kMxStages * (kA + kB);        // LDS offset of the scales
-    static constexpr int kLds = kScales + 4 * kMxScaleBytes;
+    static constexpr int kScaleA = BM * 32, kScaleB = BN * 32;   // bytes of a scale buffer
+    static constexpr int kLds = kScales + 2 * (kScaleA + kScaleB);
+    // scale loads per wave in one of a buffer's two parts; one of two waves' worth of both
+    // operands when a part is 64 rows
+    static_assert(TM == TN && (TM == 4 || TM == 2), "scale loads are dealt for these");
+    static constexpr int kScaleLoads = TM / 2;
 };
 
 template <int N>
@@ -106,7 +109,11 @@ __global__ __launch_bounds__(256, 1) void k_mx_tiles(MxGArgs g, unsigned tiles_n
             const int q = (wid * Tile::kLoadsB + i) * 64 + lane, row = q >> 2;
             ob[i] = (uint32_t)(row * pitch) + (((q & 3) ^ ((row >> 2) & 3)) << 4);
         }
-        const uint32_t os = (uint32_t)((wid * 64 + lane) * spitch);
+        // scales: a wave's load covers 32 rows x 32 bytes; row r's 16-byte halves are exchanged where
+        // r / 8 is odd, so that 16 consecutive rows' reads of one half touch every bank once
+        const uint32_t srow0 = (uint32_t)(TM == 4 ? wid : wid & 1) * 32;
+        const int srow = (int)srow0 + (lane >> 1);
+        const uint32_t os = (uint32_t)(srow * spitch) + (((lane ^ (srow >> 3)) & 1) << 4);
 
         // load number i of stage s (an offset past the operand where there is no such stage: the
         // count of loads in flight stays fixed)
@@ -120,11 +127,19 @@ __global__ __launch_bounds__(256, 1) void k_mx_tiles(MxGArgs g, unsigned tiles_n
                 dma16(rbc, buf + Tile::kA + (uint32_t)(wid * Tile::kLoadsB + i - Tile::kLoadsA) * 1024,
                       ob[i - Tile::kLoadsA] + k);
         };
-        const auto load_scales = [&](int grp) {
-            const uint32_t buf = lds0 + Tile::kScales + (uint32_t)(grp & 1) * 2 * kMxScaleBytes + (uint32_t)wid * 1024;
-            const uint32_t k = grp * 4 < nst ? (uint32_t)grp * 16 : kOutOfRange;
-            dma16(ras, buf, os + k);
-            dma16(rbs, buf + kMxScaleBytes, os + k);
+        // part 0 or 1 (half the rows) of the scales of eight stages
+        const auto load_scales = [&](int grp, int part) {
+            const uint32_t buf = lds0 + Tile::kScales + (uint32_t)(grp & 1) * (Tile::kScaleA + Tile::kScaleB);
+            const uint32_t row = (uint32_t)part * (Tile::BM / 2), at = (row + srow0) * 32;
+            const uint32_t k = grp * 8 < nst ? os + row * (uint32_t)spitch + (uint32_t)grp * 32 : kOutOfRange;
+            if constexpr (TM == 4) {
+                dma16(ras, buf + at, k);
+                dma16(rbs, buf + Tile::kScaleA + at, k);
+            } else if (wid < 2) {
+                dma16(ras, buf + at, k);
+            } else {
+                dma16(rbs, buf + Tile::kScaleA + at, k);
+            }
         };
         const auto frag = [&](int s, bool b, int tile, int j) -> int4v {
             const int row = (b ? wn * (Tile::BN / 2) : wm * (Tile::BM / 2)) + tile * 32 + li;
@@ -134,12 +149,14 @@ __global__ __launch_bounds__(256, 1) void k_mx_tiles(MxGArgs g, unsigned tiles_n
         };
         const auto scale = [&](int s, bool b, int tile) -> int {
             const int row = (b ? wn * (Tile::BN / 2) : wm * (Tile::BM / 2)) + tile * 32 + li;
-            const uint8_t* p = lds + Tile::kScales + ((s >> 2) & 1) * 2 * kMxScaleBytes +
-                               (b ? kMxScaleBytes : 0) + row * 16 + (s & 3) * 4 + 2 * h;
+            const uint8_t* p = lds + Tile::kScales + ((s >> 3) & 1) * (Tile::kScaleA + Tile::kScaleB) +
+                               (b ? Tile::kScaleA : 0) + row * 32 + ((((s >> 2) ^ (row >> 3)) & 1) << 4) +
+                               (s & 3) * 4 + 2 * h;
             return *(const uint16_t*)p;
         };
 
-        load_scales(0);
+        load_scales(0, 0);
+        load_scales(0, 1);
         static_for<0, Tile::kLoads>([&](auto i) { load_codes(0, i); });
         static_for<0, Tile::kLoads>([&](auto i) { load_codes(1, i); });
         static_for<0, Tile::kLoads>([&](auto i) { load_codes(2, i); });
@@ -167,7 +184,7 @@ __global__ __launch_bounds__(256, 1) void k_mx_tiles(MxGArgs g, unsigned tiles_n
             });
             // stage s + 1 has landed; in flight: stage s + 2, and the scales issued a stage (Q 1)
             // or two stages (Q 2) ago
-            wait_loads_and_barrier<Tile::kLoads + (Q == 1 || Q == 2 ? 2 : 0)>();
+            wait_loads_and_barrier<Tile::kLoads + (Q == 1 || Q == 2 ? Tile::kScaleLoads : 0)>();
             // second half: multiply chunk 1; issue the loads of stage s + 3 and read chunk 0 of s + 1
             static_for<0, TM * TN>([&](auto mc) {
                 constexpr int m = decltype(mc)::value, i = m / TN, j = m % TN;
@@ -182,7 +199,7 @@ __global__ __launch_bounds__(256, 1) void k_mx_tiles(MxGArgs g, unsigned tiles_n
             });
             if constexpr (TM * TN < Tile::kLoads || TM * TN < TM + TN)
                 static_assert(TM * TN >= TM + TN && TM * TN >= Tile::kLoads, "a half-stage hides its loads");
-            if constexpr (Q == 0) load_scales(s / 4 + 1);
+            if constexpr (Q == 0) load_scales(s / 8 + 1, (s >> 2) & 1);
 #pragma unroll
             for (int i = 0; i < TM; ++i) sa[i] = na[i];
 #pragma unroll
