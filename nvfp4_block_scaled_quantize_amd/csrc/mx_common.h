@@ -292,6 +292,7 @@ struct MxGArgs {
     int64_t ldc;
     const int32_t* offsets;
     int n_groups;
+    bool stream;                // float32 C past the caches
 };
 
 // A product with few rows (mx_few.hip): A packed (x null), or x to quantize rowwise.
@@ -342,17 +343,18 @@ __device__ __forceinline__ void put_c4(uint16_t* p, float a, float b, float c, f
     typedef __bf16 bf16x4v __attribute__((ext_vector_type(4)));
     *(bf16x4v*)p = bf16x4v{(__bf16)a, (__bf16)b, (__bf16)c, (__bf16)d};
 }
-// 16 bytes of a row of C, of which `left` elements exist; bfloat16 past the caches.
-__device__ __forceinline__ void stream_c(float* p, int4v v, int64_t left) {
+// 16 bytes of a row of C, of which `left` elements exist; bfloat16 always past the caches.
+__device__ __forceinline__ void store_c16(float* p, int4v v, int64_t left, bool stream) {
     if (left >= 4) {
-        *(int4_by4*)p = v;
+        if (stream) __builtin_nontemporal_store((int4_by4)v, (int4_by4*)p);
+        else *(int4_by4*)p = v;
     } else {
 #pragma unroll
         for (int i = 0; i < 3; ++i)
             if (i < left) p[i] = __int_as_float(v[i]);
     }
 }
-__device__ __forceinline__ void stream_c(uint16_t* p, int4v v, int64_t left) {
+__device__ __forceinline__ void store_c16(uint16_t* p, int4v v, int64_t left, bool) {
     if (left >= 8) {
         __builtin_nontemporal_store((int4_by2)v, (int4_by2*)p);
     } else {

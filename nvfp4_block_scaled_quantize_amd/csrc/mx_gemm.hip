@@ -222,9 +222,6 @@ __global__ __launch_bounds__(256, 1) void k_mx_tiles(MxGArgs g, unsigned tiles_n
     // 32 x 32: a wave puts 32 rows of its part of C into LDS (its own piece, behind the barrier
     // that ends the stages' use of it) and stores them from there 16 bytes a lane, a row's 128 or
     // 64 columns contiguous.
-    // bfloat16 stores stream past the caches (grouped 16384 x 4096 x 2048: 122 us against 132 with
-    // ordinary ones, and no slower where a quantizer reads C back: 8192 x 9216 x 4096 220 us
-    // either way); float32 ones do not (78 against 88 us with such a reader).
     asm volatile("s_barrier" ::: "memory");
     constexpr int kCols = TN * 32, kRowBytes = kCols * (int)sizeof(T) + 16;
     constexpr int kPer = 16 / (int)sizeof(T), kLanes = kCols / kPer, kRowsAtOnce = 64 / kLanes;
@@ -244,7 +241,7 @@ __global__ __launch_bounds__(256, 1) void k_mx_tiles(MxGArgs g, unsigned tiles_n
         for (int k = 0; k < 32 / kRowsAtOnce; ++k) {
             const int4v v = *(const int4v*)(piece + (k * kRowsAtOnce + lane / kLanes) * kRowBytes + (lane % kLanes) * 16);
             const int64_t row = row0 + k * kRowsAtOnce;
-            if (row < m1) stream_c(c + row * g.ldc + col, v, g.N - col);
+            if (row < m1) store_c16(c + row * g.ldc + col, v, g.N - col, g.stream);
         }
     }
 }
@@ -266,8 +263,15 @@ static int launch_tiles(const MxGArgs& g, hipStream_t st) {
     return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
 }
 
+// How C is stored.  bfloat16 streams past the caches (grouped 16384 x 4096 x 2048 99 us against
+// 103 with ordinary stores, and about the same where a quantizer reads C back: 8192 x 9216 x
+// 4096 190 against 186 us, 2048 x 4096 x 2048 20.7 against 22.7).  float32 does where little of C
+// would still be in the last-level cache (256 MB) for its reader: 15 gradients of 4096 x 2048
+// (503 MB) 130 against 171 us, 15 of 1536 x 2048 (189 MB) 49.5 against 53.2; but 134 MB with a
+// reader 84 against 74.
 template <int MODE>
-static int launch_gemm(const MxGArgs& g, int c_dtype, hipStream_t st) {
+static int launch_gemm(MxGArgs g, int c_dtype, hipStream_t st) {
+    g.stream = g.M * g.N * 4 * (MODE == MxK ? g.n_groups : 1) >= ((int64_t)160 << 20);
     const int64_t groups = MODE == MxK ? g.n_groups : 1;
     const int64_t big = ((g.M + 255) / 256) * ((g.N + 255) / 256) * groups;
     const int64_t small = ((g.M + 127) / 128) * ((g.N + 127) / 128) * groups;
@@ -305,7 +309,7 @@ extern "C" int mxfp4_gemm(const mxfp4_tensor* a, const mxfp4_tensor* b, int64_t 
     bool empty;
     if (int rc = check_gemm(a, b, M, N, K, c, c_dtype, ldc, &empty)) return rc;
     if (empty) return NVFP4_OK;
-    const MxGArgs g = {a->codes, a->scales, b->codes, b->scales, M, N, mx_pad(K), 0, c, ldc, nullptr, 0};
+    const MxGArgs g = {a->codes, a->scales, b->codes, b->scales, M, N, mx_pad(K), 0, c, ldc, nullptr, 0, false};
     // Up to 16 rows go to the kernel that streams B once (16 x 6144 x 4096 7.3 us against 10.9).
     if (M <= 16 && mx_few_fits(M, g.kp)) return mx_few_packed({g, nullptr, 0, K, 0}, c_dtype, (hipStream_t)stream);
     return launch_gemm<MxDense>(g, c_dtype, (hipStream_t)stream);
@@ -320,7 +324,7 @@ extern "C" int mxfp4_gemm_grouped(const mxfp4_tensor* a, const mxfp4_tensor* b, 
     if (int rc = mx_check_groups(offsets, n_groups, M)) return rc;
     if (empty) return NVFP4_OK;
     const MxGArgs g = {a->codes, a->scales, b->codes, b->scales, M, N, mx_pad(K), 0, c, ldc,
-                       offsets, (int)n_groups};
+                       offsets, (int)n_groups, false};
     return launch_gemm<MxRows>(g, c_dtype, (hipStream_t)stream);
 }
 
@@ -334,7 +338,7 @@ extern "C" int mxfp4_gemm_grouped_wgrad(const mxfp4_tensor* a, const mxfp4_tenso
     if (int rc = check_gemm(a, b, M, N, kp, c, c_dtype, ldc, &empty)) return rc;
     if (empty) return NVFP4_OK;
     const MxGArgs g = {a->codes, a->scales, b->codes, b->scales, M, N, kp, rows, c, ldc,
-                       offsets, (int)n_groups};
+                       offsets, (int)n_groups, false};
     return launch_gemm<MxK>(g, c_dtype, (hipStream_t)stream);
 }
 
@@ -377,7 +381,7 @@ extern "C" int mxfp4_linear(const void* x, int dtype, int64_t M, int64_t K, int6
         if (ld_x < K) return NVFP4_ERR_SHAPE;
         if (scale_rule != MXFP4_SCALE_FLOOR && scale_rule != MXFP4_SCALE_CEIL) return NVFP4_ERR_MODE;
         if (empty) return NVFP4_OK;
-        const MxFArgs f = {{nullptr, nullptr, w->codes, w->scales, M, N, mx_pad(K), 0, c, ldc, offsets, (int)n_groups},
+        const MxFArgs f = {{nullptr, nullptr, w->codes, w->scales, M, N, mx_pad(K), 0, c, ldc, offsets, (int)n_groups, false},
                            x, ld_x, K, mx_above(scale_rule)};
         return mx_few_linear(f, dtype, c_dtype, (hipStream_t)stream);
     }
