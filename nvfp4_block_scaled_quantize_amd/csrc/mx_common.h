@@ -292,7 +292,6 @@ struct MxGArgs {
     int64_t ldc;
     const int32_t* offsets;
     int n_groups;
-    bool stream;                // float32 C past the caches
 };
 
 // A product with few rows (mx_few.hip): A packed (x null), or x to quantize rowwise.
@@ -343,24 +342,20 @@ __device__ __forceinline__ void put_c4(uint16_t* p, float a, float b, float c, f
     typedef __bf16 bf16x4v __attribute__((ext_vector_type(4)));
     *(bf16x4v*)p = bf16x4v{(__bf16)a, (__bf16)b, (__bf16)c, (__bf16)d};
 }
-// 16 bytes of a row of C, of which `left` elements exist; bfloat16 always past the caches.
-__device__ __forceinline__ void store_c16(float* p, int4v v, int64_t left, bool stream) {
-    if (left >= 4) {
-        if (stream) __builtin_nontemporal_store((int4_by4)v, (int4_by4*)p);
-        else *(int4_by4*)p = v;
+// 16 bytes of a row of C, of which `left` elements exist.  STREAM: past the caches.
+template <bool STREAM, typename T>
+__device__ __forceinline__ void store_c16(T* p, int4v v, int64_t left) {
+    using Vec = typename Oct<T>::Vec;
+    constexpr int n = 16 / (int)sizeof(T);
+    if (left >= n) {
+        if constexpr (STREAM) __builtin_nontemporal_store((Vec)v, (Vec*)p);
+        else *(Vec*)p = v;
     } else {
+        T e[n];
+        __builtin_memcpy(e, &v, sizeof(e));
 #pragma unroll
-        for (int i = 0; i < 3; ++i)
-            if (i < left) p[i] = __int_as_float(v[i]);
-    }
-}
-__device__ __forceinline__ void store_c16(uint16_t* p, int4v v, int64_t left, bool) {
-    if (left >= 8) {
-        __builtin_nontemporal_store((int4_by2)v, (int4_by2*)p);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 7; ++i)
-            if (i < left) p[i] = (uint16_t)((uint32_t)v[i >> 1] >> (16 * (i & 1)));
+        for (int i = 0; i < n - 1; ++i)
+            if (i < left) p[i] = e[i];
     }
 }
 

@@ -48,7 +48,7 @@ __device__ __forceinline__ void wait_loads_and_barrier() {
     asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
-template <typename T, int MODE, int TM, int TN>
+template <typename T, int MODE, int TM, int TN, bool STREAM>
 __global__ __launch_bounds__(256, 1) void k_mx_tiles(MxGArgs g, unsigned tiles_n, unsigned tiles_m) {
     using Tile = MxTile<TM, TN>;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
@@ -241,12 +241,12 @@ __global__ __launch_bounds__(256, 1) void k_mx_tiles(MxGArgs g, unsigned tiles_n
         for (int k = 0; k < 32 / kRowsAtOnce; ++k) {
             const int4v v = *(const int4v*)(piece + (k * kRowsAtOnce + lane / kLanes) * kRowBytes + (lane % kLanes) * 16);
             const int64_t row = row0 + k * kRowsAtOnce;
-            if (row < m1) store_c16(c + row * g.ldc + col, v, g.N - col, g.stream);
+            if (row < m1) store_c16<STREAM>(c + row * g.ldc + col, v, g.N - col);
         }
     }
 }
 
-template <typename T, int MODE, int TM, int TN>
+template <typename T, int MODE, int TM, int TN, bool STREAM>
 static int launch_tiles(const MxGArgs& g, hipStream_t st) {
     using Tile = MxTile<TM, TN>;
     const int64_t tn = (g.N + Tile::BN - 1) / Tile::BN, tm = (g.M + Tile::BM - 1) / Tile::BM;
@@ -256,7 +256,7 @@ static int launch_tiles(const MxGArgs& g, hipStream_t st) {
     if (MODE == MxK) tiles *= g.n_groups;
     static_assert(Tile::kLds <= kMxMaxLds, "LDS budget");
     if (!mx_grid_fits(tiles, 256)) return NVFP4_ERR_SHAPE;
-    const auto kernel = k_mx_tiles<T, MODE, TM, TN>;
+    const auto kernel = k_mx_tiles<T, MODE, TM, TN, STREAM>;
     static std::atomic<uint64_t> ready{0};
     if (int rc = mx_allow_lds((const void*)kernel, Tile::kLds, ready)) return rc;
     kernel<<<dim3((unsigned)tiles), 256, Tile::kLds, st>>>(g, (unsigned)tn, (unsigned)tm);
@@ -269,9 +269,16 @@ static int launch_tiles(const MxGArgs& g, hipStream_t st) {
 // would still be in the last-level cache (256 MB) for its reader: 15 gradients of 4096 x 2048
 // (503 MB) 130 against 171 us, 15 of 1536 x 2048 (189 MB) 49.5 against 53.2; but 134 MB with a
 // reader 84 against 74.
+template <int MODE, int TM, int TN>
+static int launch_c(const MxGArgs& g, int c_dtype, hipStream_t st) {
+    if (c_dtype == NVFP4_BF16) return launch_tiles<uint16_t, MODE, TM, TN, true>(g, st);
+    const int64_t bytes = g.M * g.N * 4 * (MODE == MxK ? g.n_groups : 1);
+    return bytes >= ((int64_t)160 << 20) ? launch_tiles<float, MODE, TM, TN, true>(g, st)
+                                         : launch_tiles<float, MODE, TM, TN, false>(g, st);
+}
+
 template <int MODE>
-static int launch_gemm(MxGArgs g, int c_dtype, hipStream_t st) {
-    g.stream = g.M * g.N * 4 * (MODE == MxK ? g.n_groups : 1) >= ((int64_t)160 << 20);
+static int launch_gemm(const MxGArgs& g, int c_dtype, hipStream_t st) {
     const int64_t groups = MODE == MxK ? g.n_groups : 1;
     const int64_t big = ((g.M + 255) / 256) * ((g.N + 255) / 256) * groups;
     const int64_t small = ((g.M + 127) / 128) * ((g.N + 127) / 128) * groups;
@@ -279,11 +286,8 @@ static int launch_gemm(MxGArgs g, int c_dtype, hipStream_t st) {
     // 31 us at K = 4096), so the smaller tile wins where it wastes less of the last round:
     // 2048 x 2048 x 4096 15 against 31 us, 1024 x 6144 x 4096 24 against 31; but 4096^3 52
     // against 43 and 8192^3 378 against 284.
-    if (((small + 255) / 256) * 46 < ((big + 255) / 256) * 100)
-        return c_dtype == NVFP4_BF16 ? launch_tiles<uint16_t, MODE, 2, 2>(g, st)
-                                     : launch_tiles<float, MODE, 2, 2>(g, st);
-    return c_dtype == NVFP4_BF16 ? launch_tiles<uint16_t, MODE, 4, 4>(g, st)
-                                 : launch_tiles<float, MODE, 4, 4>(g, st);
+    if (((small + 255) / 256) * 46 < ((big + 255) / 256) * 100) return launch_c<MODE, 2, 2>(g, c_dtype, st);
+    return launch_c<MODE, 4, 4>(g, c_dtype, st);
 }
 
 // Checks shared by the products; *empty when C has no elements.
@@ -309,7 +313,7 @@ extern "C" int mxfp4_gemm(const mxfp4_tensor* a, const mxfp4_tensor* b, int64_t 
     bool empty;
     if (int rc = check_gemm(a, b, M, N, K, c, c_dtype, ldc, &empty)) return rc;
     if (empty) return NVFP4_OK;
-    const MxGArgs g = {a->codes, a->scales, b->codes, b->scales, M, N, mx_pad(K), 0, c, ldc, nullptr, 0, false};
+    const MxGArgs g = {a->codes, a->scales, b->codes, b->scales, M, N, mx_pad(K), 0, c, ldc, nullptr, 0};
     // Up to 16 rows go to the kernel that streams B once (16 x 6144 x 4096 7.3 us against 10.9).
     if (M <= 16 && mx_few_fits(M, g.kp)) return mx_few_packed({g, nullptr, 0, K, 0}, c_dtype, (hipStream_t)stream);
     return launch_gemm<MxDense>(g, c_dtype, (hipStream_t)stream);
@@ -324,7 +328,7 @@ extern "C" int mxfp4_gemm_grouped(const mxfp4_tensor* a, const mxfp4_tensor* b, 
     if (int rc = mx_check_groups(offsets, n_groups, M)) return rc;
     if (empty) return NVFP4_OK;
     const MxGArgs g = {a->codes, a->scales, b->codes, b->scales, M, N, mx_pad(K), 0, c, ldc,
-                       offsets, (int)n_groups, false};
+                       offsets, (int)n_groups};
     return launch_gemm<MxRows>(g, c_dtype, (hipStream_t)stream);
 }
 
@@ -338,7 +342,7 @@ extern "C" int mxfp4_gemm_grouped_wgrad(const mxfp4_tensor* a, const mxfp4_tenso
     if (int rc = check_gemm(a, b, M, N, kp, c, c_dtype, ldc, &empty)) return rc;
     if (empty) return NVFP4_OK;
     const MxGArgs g = {a->codes, a->scales, b->codes, b->scales, M, N, kp, rows, c, ldc,
-                       offsets, (int)n_groups, false};
+                       offsets, (int)n_groups};
     return launch_gemm<MxK>(g, c_dtype, (hipStream_t)stream);
 }
 
@@ -381,7 +385,7 @@ extern "C" int mxfp4_linear(const void* x, int dtype, int64_t M, int64_t K, int6
         if (ld_x < K) return NVFP4_ERR_SHAPE;
         if (scale_rule != MXFP4_SCALE_FLOOR && scale_rule != MXFP4_SCALE_CEIL) return NVFP4_ERR_MODE;
         if (empty) return NVFP4_OK;
-        const MxFArgs f = {{nullptr, nullptr, w->codes, w->scales, M, N, mx_pad(K), 0, c, ldc, offsets, (int)n_groups, false},
+        const MxFArgs f = {{nullptr, nullptr, w->codes, w->scales, M, N, mx_pad(K), 0, c, ldc, offsets, (int)n_groups},
                            x, ld_x, K, mx_above(scale_rule)};
         return mx_few_linear(f, dtype, c_dtype, (hipStream_t)stream);
     }
