@@ -277,17 +277,22 @@ static int launch_c(const MxGArgs& g, int c_dtype, hipStream_t st) {
                                          : launch_tiles<float, MODE, TM, TN, false>(g, st);
 }
 
+// Which tile.  256 x 256 tiles run one to a compute unit, 256 at a time; 128 x 128 tiles two to a
+// unit.  In percent of a round of the large ones, 512 small ones take 68 and up to 256 of them 45
+// (8192^3: 4 rounds 249 us against 8 351 us; 2048 x 2048 x 4096 with 256 small tiles 11.3 us), so
+// the small tile wins where the large ones' last round would be mostly empty: 2048 x 9216 x 4096
+// (288 large tiles) 51 against 58 us, 1024 x 6144 x 4096 (96) 18 against 24, but 1024 x 9216 x
+// 4096 (144 large, 576 small) 30 against 25.  Groups of rows end in half a tile on average.
 template <int MODE>
 static int launch_gemm(const MxGArgs& g, int c_dtype, hipStream_t st) {
-    const int64_t groups = MODE == MxK ? g.n_groups : 1;
-    const int64_t big = ((g.M + 255) / 256) * ((g.N + 255) / 256) * groups;
-    const int64_t small = ((g.M + 127) / 128) * ((g.N + 127) / 128) * groups;
-    // A full round of 256 tiles of 128 x 128 takes 0.46 of the time of one of 256 x 256 (15 and
-    // 31 us at K = 4096), so the smaller tile wins where it wastes less of the last round:
-    // 2048 x 2048 x 4096 15 against 31 us, 1024 x 6144 x 4096 24 against 31; but 4096^3 52
-    // against 43 and 8192^3 378 against 284.
-    if (((small + 255) / 256) * 46 < ((big + 255) / 256) * 100) return launch_c<MODE, 2, 2>(g, c_dtype, st);
-    return launch_c<MODE, 4, 4>(g, c_dtype, st);
+    const auto tiles = [&](int64_t side) {
+        int64_t m = (g.M + side - 1) / side;
+        if (MODE == MxRows) m = (2 * g.M / side + (g.n_groups < g.M ? g.n_groups : g.M) + 1) / 2;
+        return m * ((g.N + side - 1) / side) * (MODE == MxK ? g.n_groups : 1);
+    };
+    const int64_t big = (tiles(256) + 255) / 256 * 100, n = tiles(128), rest = n % 512;
+    const int64_t small = n / 512 * 68 + (rest == 0 ? 0 : rest <= 256 ? 45 : 68);
+    return small < big ? launch_c<MODE, 2, 2>(g, c_dtype, st) : launch_c<MODE, 4, 4>(g, c_dtype, st);
 }
 
 // Checks shared by the products; *empty when C has no elements.
