@@ -251,19 +251,9 @@ __device__ __forceinline__ void mx_tile_of(unsigned bid, unsigned tiles_m, unsig
 }
 
 // The tile of workgroup `bid` when the rows are grouped: tiles_n columns of units.  False past
-// the last unit (grids are sized for the worst offsets).  With up to 64 groups the offsets are
-// read and scanned once.
-__device__ __forceinline__ bool mx_find_tile(const int32_t* offsets, int n_groups, int rows, int unit,
-                                             unsigned bid, unsigned tiles_n, unsigned& tm, unsigned& tn,
-                                             MxUnit& out) {
-    if (n_groups > 64) {
-        const unsigned units = (unsigned)mx_units(offsets, n_groups, rows, unit);
-        if (bid >= units * tiles_n) return false;
-        mx_tile_of(bid, units, tiles_n, tm, tn);
-        mx_find_unit(offsets, n_groups, rows, unit, tm, out);
-        return true;
-    }
-    const MxSpan x = mx_span(offsets, n_groups, rows, unit, 0, 0);
+// the last unit (grids are sized for the worst offsets).  x: the span of all (at most 64) groups.
+__device__ __forceinline__ bool mx_span_tile(const MxSpan& x, int n_groups, int rows, int unit, unsigned bid,
+                                             unsigned tiles_n, unsigned& tm, unsigned& tn, MxUnit& out) {
     const int grouped = lane_value(x.p, 63), end = lane_value(x.e, 63);
     const unsigned units = (unsigned)(grouped + (rows - end + unit - 1) / unit);
     if (bid >= units * tiles_n) return false;
@@ -278,6 +268,28 @@ __device__ __forceinline__ bool mx_find_tile(const int32_t* offsets, int n_group
     out.row0 = gs + (tm - out.first) * unit;
     out.rows = ge - out.row0 < unit ? ge - out.row0 : unit;
     return true;
+}
+
+// mx_group from the span of all (at most 64) groups.
+__device__ __forceinline__ void mx_span_group(const MxSpan& x, int g, MxUnit& out) {
+    out.group = g;
+    out.first = lane_value(x.p - x.n, g);
+    out.group_row0 = out.row0 = lane_value(x.s, g);
+    out.group_rows = out.rows = lane_value(x.e, g) - out.row0;
+}
+
+// mx_span_tile for any number of groups: with up to 64 the offsets are read and scanned once.
+__device__ __forceinline__ bool mx_find_tile(const int32_t* offsets, int n_groups, int rows, int unit,
+                                             unsigned bid, unsigned tiles_n, unsigned& tm, unsigned& tn,
+                                             MxUnit& out) {
+    if (n_groups > 64) {
+        const unsigned units = (unsigned)mx_units(offsets, n_groups, rows, unit);
+        if (bid >= units * tiles_n) return false;
+        mx_tile_of(bid, units, tiles_n, tm, tn);
+        mx_find_unit(offsets, n_groups, rows, unit, tm, out);
+        return true;
+    }
+    return mx_span_tile(mx_span(offsets, n_groups, rows, unit, 0, 0), n_groups, rows, unit, bid, tiles_n, tm, tn, out);
 }
 
 // ---------------------------------------------------------------- products
@@ -319,6 +331,22 @@ inline int mx_allow_lds(const void* kernel, int bytes, std::atomic<uint64_t>& re
         return NVFP4_ERR_HIP;
     ready.fetch_or(bit, std::memory_order_relaxed);
     return NVFP4_OK;
+}
+
+// The 256 x 256 tiles (mx_tile256.hip).  mode: MxDense, MxRows, MxK; stream: float32 C past the
+// caches.
+int mx_tile256(const MxGArgs& g, int mode, int c_dtype, bool stream, hipStream_t st);
+
+// Compute units of the current device, rounded down to a multiple of the 8 XCDs; 0 on an error.
+inline int mx_compute_units() {
+    static std::atomic<int> known[64];
+    int dev = 0, n = 0;
+    if (hipGetDevice(&dev) != hipSuccess) return 0;
+    if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed))) return n;
+    if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess) return 0;
+    n = n > 8 ? n / 8 * 8 : 8;
+    if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+    return n;
 }
 
 // A grid's threads are counted in 32 bits.

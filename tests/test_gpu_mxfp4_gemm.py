@@ -78,6 +78,12 @@ def test_dense(nv, M, N, K):
         assert (buf == 3.0).all()
 
 
+@pytest.mark.parametrize("M,N,K", [(6144, 5000, 640), (6100, 4990, 130), (5000, 4100, 1500), (6144, 5120, 257)])
+def test_dense_more_tiles_than_compute_units(nv, M, N, K):
+    """Workgroups that go through several large tiles, whole ones and ones cut at C's edges."""
+    test_dense(nv, M, N, K)
+
+
 def test_scales_far_apart_and_nan(nv):
     """Block scales from 2^-60 to 2^60; a NaN scale reaches exactly its row or column."""
     a, b = copy_of(nv, (70,), 500, 3, spread=60), copy_of(nv, (90,), 500, 4, spread=60)
@@ -120,9 +126,24 @@ GROUPED = [(1, 3, 40, 96, [0, 0, 1, 1]), (24, 8, 300, 500, spread_offsets(24, 8,
            (64, 2, 65, 64, [0, 0, 0]), (300, 3, 100, 64, [5, 900, 2, 300]), (4000, 6, 300, 700, spread_offsets(4000, 6, 4))]
 
 
-@pytest.mark.parametrize("case", range(len(GROUPED)))
+def many_offsets(rows, groups, seed, tail=0):
+    """Every third group empty."""
+    off = spread_offsets(rows, groups, seed, tail)
+    for g in range(1, groups, 3):
+        off[g] = off[g - 1]
+    return off
+
+
+# more large tiles than compute units: several per workgroup, some without anything to multiply
+GROUPED_MANY = [(6000, 5, 4600, 300, [0, 2000, 2000, 2600, 2601, 5500]), (20000, 70, 2100, 200, many_offsets(20000, 70, 7, 100)),
+                (6144, 4, 4608, 512, [0, 1536, 3072, 4608, 6144])]
+WGRAD_MANY = [(3000, 9, 1500, 1536, [0, 0, 100, 1300, 1300, 1428, 2000, 2001, 2500, 3000]),
+              (9000, 120, 500, 512, many_offsets(9000, 120, 8, 50))]
+
+
+@pytest.mark.parametrize("case", range(len(GROUPED) + len(GROUPED_MANY)))
 def test_grouped_rows(nv, case):
-    M, G, N, K, off = GROUPED[case]
+    M, G, N, K, off = (GROUPED + GROUPED_MANY)[case]
     print(f"grouped rows {case}", flush=True)
     a, b = copy_of(nv, (M,), K, 5), copy_of(nv, (G, N), K, 6)
     offsets = torch.tensor(off, dtype=torch.int32, device=dev())
@@ -138,9 +159,9 @@ def test_grouped_rows(nv, case):
         assert torch.isnan(buf[0]).all() and torch.isnan(buf[-1]).all() and torch.isnan(buf[:, N:]).all()
 
 
-@pytest.mark.parametrize("case", range(len(GROUPED)))
+@pytest.mark.parametrize("case", range(len(GROUPED) + len(WGRAD_MANY)))
 def test_grouped_wgrad(nv, case):
-    rows, G, N, K, off = GROUPED[case]
+    rows, G, N, K, off = (GROUPED + WGRAD_MANY)[case]
     print(f"grouped wgrad {case}", flush=True)
     g = torch.Generator(device=dev()).manual_seed(case)
     x = torch.randn(rows, K, generator=g, device=dev())
