@@ -10,9 +10,9 @@
 // of K at 32 (l / 16), with their scale byte.
 //
 // Measured (GPU time per call in a replayed graph, three sets of operands in turn): 1 x 6144 x
-// 4096, x in bfloat16, 6.8 us (W alone at the card's copy rate: 2.8 us, an empty kernel: about
-// 2.4 us) against 13.0 us as quantize and tiled product; 16 rows 10.5 us, packed, the quantize
-// included, against 14.1 us.
+// 4096, x in bfloat16, 5.7 us (W alone at the card's copy rate: 2.8 us, an empty kernel: about
+// 2.4 us) against 13.0 us as quantize and tiled product; 16 rows 9.4 us, packed, the quantize
+// included, against 14.1 us; 24 rows over 17 groups (4096 x 2048, 71 MB of W) 16.6 us.
 #include "mx_common.h"
 
 #include <atomic>
@@ -20,7 +20,7 @@
 namespace nvfp4 {
 
 constexpr int kFewRows = 16;
-constexpr int kFewBatch = 4;                 // K steps of 128 in one batch of loads
+constexpr int kFewBatch = 4;                 // K steps of 128 in one batch of loads (of scales: 16 bytes)
 // LDS row strides of A: 64 and 4 bytes past the row, so that 16 rows' reads spread over the banks
 __host__ __device__ constexpr int few_code_stride(int kp) { return kp / 2 + 64; }
 __host__ __device__ constexpr int few_scale_stride(int kp) { return kp / 32 + 4; }
@@ -57,16 +57,24 @@ __global__ __launch_bounds__(64 * WAVES) void k_mx_few(MxFArgs f, unsigned tiles
     const uint8_t* ws = bs + n * spitch;
     const int s0 = steps * part / kSplit, s1 = steps * (part + 1) / kSplit;
 
+    // A load of 16 rows costs the address unit as much for 4 bytes a row as for 64, so a batch's
+    // scales come in one, unless that would reach past the row's end.
     struct Batch {
         int4v w[kFewBatch];
         int s[kFewBatch];
     };
     const auto load = [&](Batch& b, int s) {
 #pragma unroll
-        for (int i = 0; i < kFewBatch; ++i) {
-            const int64_t at = s + i < s1 ? s + i : s1 - 1;     // past the wave's part: not used
-            b.w[i] = *(const int4v*)(wc + at * 64);
-            b.s[i] = *(const int*)(ws + at * 4);
+        for (int i = 0; i < kFewBatch; ++i)
+            if (s + i < s1) b.w[i] = *(const int4v*)(wc + (int64_t)(s + i) * 64);
+        if (s + kFewBatch <= steps) {
+            const int4v v = *(const int4_by4*)(ws + (int64_t)s * 4);
+#pragma unroll
+            for (int i = 0; i < kFewBatch; ++i) b.s[i] = v[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < kFewBatch; ++i)
+                if (s + i < s1) b.s[i] = *(const int*)(ws + (int64_t)(s + i) * 4);
         }
     };
     // The first of x is asked for before W: loads return in order, and x has to be quantized
@@ -76,8 +84,13 @@ __global__ __launch_bounds__(64 * WAVES) void k_mx_few(MxFArgs f, unsigned tiles
         const int r = i / per, k = (i - r * per) * 8;
         if constexpr (sizeof(XT) > 1) return load_oct((const XT*)f.x + (m0 + r) * f.ldx + k, i < octs ? f.K - k : 0);
     };
-    [[maybe_unused]] Oct<XT> o;
-    if constexpr (sizeof(XT) > 1) o = load_x(t);
+    constexpr int kAhead = 4;
+    [[maybe_unused]] Oct<XT> o[kAhead];
+    if constexpr (sizeof(XT) > 1) {
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+            if (j * kThreads < octs) o[j] = load_x(t + j * kThreads);
+    }
     Batch cur = {};
     if (s0 < s1) load(cur, s0);
 
@@ -94,15 +107,18 @@ __global__ __launch_bounds__(64 * WAVES) void k_mx_few(MxFArgs f, unsigned tiles
                 *(uint32_t*)(as + r * sstride + i * 4) = *(const uint32_t*)(g.as + (m0 + r) * spitch + i * 4);
         }
     } else {
-        for (int i = t; i < octs;) {
+        const auto put_x = [&](int i, const Oct<XT>& x) {
             const int r = i / per, k = (i - r * per) * 8;
-            const uint32_t code = mx_scale_code(quad_max(max_bits(o)), f.above);
-            const uint32_t w = codes_rne(o, mx_scale_value(code));
+            const uint32_t code = mx_scale_code(quad_max(max_bits(x)), f.above);
+            const uint32_t w = codes_rne(x, mx_scale_value(code));
+            if (i >= octs) return;
             *(uint32_t*)(ac + r * cstride + k / 2) = code == 255u ? 0u : w;
             if ((t & 3) == 0) as[r * sstride + k / 32] = (uint8_t)code;
-            i += kThreads;
-            if (i < octs) o = load_x(i);
-        }
+        };
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+            if (j * kThreads < octs) put_x(t + j * kThreads, o[j]);
+        for (int i = t + kAhead * kThreads; i - t < octs; i += kThreads) put_x(i, load_x(i));
     }
     __syncthreads();
 
@@ -159,7 +175,8 @@ static int launch(const MxFArgs& f, int64_t units, hipStream_t st) {
 
 // Dense: 16 columns a workgroup.  Eight waves halve a wave's K (1 x 1024 x 8192 6.4 against 7.0
 // us, 16 x 6144 x 4096 10.5 against 11.8), but past about 448 workgroups their launch becomes
-// the bound (4 x 9216 x 2048 8.6 against 6.8 us with four).
+// the bound (4 x 9216 x 2048 8.6 against 6.8 us with four).  (These and the figures below are
+// from before a batch's scales came in one load, which took a sixth off every one of them.)
 template <typename T, typename XT>
 static int launch_dense(const MxFArgs& f, hipStream_t st) {
     if ((f.g.N + 15) / 16 > 448) return launch<T, XT, MxDense, 16, 4>(f, 1, st);
