@@ -336,6 +336,8 @@ inline int mx_allow_lds(const void* kernel, int bytes, std::atomic<uint64_t>& re
 // The 256 x 256 tiles (mx_tile256.hip).  mode: MxDense, MxRows, MxK; stream: float32 C past the
 // caches.
 int mx_tile256(const MxGArgs& g, int mode, int c_dtype, bool stream, hipStream_t st);
+// The same with 128 x 128 tiles (mx_tile128.hip).
+int mx_tile128(const MxGArgs& g, int mode, int c_dtype, bool stream, hipStream_t st);
 
 // Compute units of the current device, rounded down to a multiple of the 8 XCDs; 0 on an error.
 inline int mx_compute_units() {

@@ -35,36 +35,16 @@
 // over 29 groups 99 us; 15 gradients of 1536 x 2048 over 8192 rows 43 us (189 MB of C: 40 us at
 // the copy rate).  Bound by power and by the matrix instructions: on all compute units these
 // alone, with random operands in registers, run at 6.5 PFLOP/s (1.6 GHz) against 9.3 with zeros.
-#include "mx_common.h"
+#include "mx_tile.h"
 
 namespace nvfp4 {
 
-constexpr int kTile = 256, kRow = 128;               // tile side; code bytes a row and stage
+constexpr int kTile = 256;                           // tile side
 constexpr int kOperand = kTile * kRow, kSlot = 2 * kOperand;
 constexpr int kScaleBuf = kTile * 32;                // one operand, four stages
 constexpr int kScalesAt = 2 * kSlot;                 // LDS offset of the scale buffers
 constexpr int kTileLds = kScalesAt + 4 * kScaleBuf;
 static_assert(kTileLds <= kMxMaxLds, "LDS budget");
-constexpr uint32_t kBias = 3072;                     // see load_codes
-
-// dma16 in two: M0, and a load at an offset that moves both its addresses.  Nothing that the
-// compiler makes of these kernels writes M0.
-__device__ __forceinline__ void set_m0(uint32_t lds_addr) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0" ::"s"(lds_addr) : "memory");
-}
-template <int OFFSET>
-__device__ __forceinline__ void dma16_at(int4v rsrc, uint32_t voff, uint32_t soff) {
-    asm volatile("buffer_load_dwordx4 %0, %1, %2 offen offset:%3 lds" ::"v"(voff), "s"(rsrc), "s"(soff), "n"(OFFSET)
-                 : "memory");
-}
-
-template <int I> using Int = std::integral_constant<int, I>;
-
-template <int N>
-__device__ __forceinline__ void wait_and_barrier() {
-    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(N) : "memory");
-}
-
 // Waits for all but the ten (or, if `more`, the 42) newest operations.
 __device__ __forceinline__ void wait_10_or_42_and_barrier(bool more) {
     asm volatile("s_cmp_lg_u32 %0, 0\n\ts_cbranch_scc1 1f\n\ts_waitcnt vmcnt(10)\n1:\ts_waitcnt vmcnt(42)\n\ts_barrier"
@@ -170,7 +150,7 @@ __global__ __launch_bounds__(256, 1) void k_mx_tile256(MxGArgs g, unsigned tiles
         const int left = pk - ps * kRow;
         past[0] = chunk < left ? 0u : kOutOfRange;
         past[1] = (chunk ^ 64) < left ? 0u : kOutOfRange;
-        kat = (uint32_t)(ps * kRow);
+        kat = left > 0 ? (uint32_t)(ps * kRow) : 0u;
     };
     const auto load_codes = [&](uint32_t slot, auto nc) {
         constexpr int n = decltype(nc)::value, i = n % 8, quarter = n % 4;
