@@ -11,8 +11,8 @@
 //
 // Measured (GPU time per call in a replayed graph, three sets of operands in turn): 1 x 6144 x
 // 4096, x in bfloat16, 5.7 us (W alone at the card's copy rate: 2.8 us, an empty kernel: about
-// 2.4 us) against 13.0 us as quantize and tiled product; 16 rows 9.4 us, packed, the quantize
-// included, against 14.1 us; 24 rows over 17 groups (4096 x 2048, 71 MB of W) 16.6 us.
+// 2.4 us) against 8.4 us as quantize and packed product; 16 rows 9.5 us, packed, the quantize
+// included, against 13.7 us by tiles; 24 rows over 17 groups (4096 x 2048, 71 MB of W) 15.3 us.
 #include "mx_common.h"
 
 #include <atomic>
@@ -173,23 +173,24 @@ static int launch(const MxFArgs& f, int64_t units, hipStream_t st) {
     return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
 }
 
-// Dense: 16 columns a workgroup.  Eight waves halve a wave's K (1 x 1024 x 8192 6.4 against 7.0
-// us, 16 x 6144 x 4096 10.5 against 11.8), but past about 448 workgroups their launch becomes
-// the bound (4 x 9216 x 2048 8.6 against 6.8 us with four).  (These and the figures below are
-// from before a batch's scales came in one load, which took a sixth off every one of them.)
+// Dense: 16 columns a workgroup.  Eight waves halve a wave's K (1 x 1024 x 8192 5.3 against 6.4
+// us, 16 x 6144 x 4096 9.5 against 11.3), but with more than about 448 workgroups four are enough
+// and start sooner (1 x 16384 x 2048 5.8 against 6.2 us, 4 x 9216 x 2048 5.5 either way).
 template <typename T, typename XT>
 static int launch_dense(const MxFArgs& f, hipStream_t st) {
     if ((f.g.N + 15) / 16 > 448) return launch<T, XT, MxDense, 16, 4>(f, 1, st);
     return launch<T, XT, MxDense, 16, 8>(f, 1, st);
 }
 
-// Grouped: there are enough columns in all for 64 a workgroup, whose four waves need no split of
-// K (24 rows over 17 groups, 4096 x 2048: 21.5 us against 23.7 with 16 columns).
+// Grouped: four waves on 32 columns, two of them sharing K (24 rows over 17 groups, 4096 x 2048:
+// 15.2 us against 17.1 with 16 columns and 16.8 with 64, which need no split), or on 16 where that
+// leaves compute units without work (4 rows over 4 groups, 1024 x 2048: 3.8 us against 4.6).
 template <typename T, typename XT>
 static int launch_rows(const MxFArgs& f, hipStream_t st) {
     // every group, and the rows in none, may end in a partial unit
     const int64_t units = f.g.M / kFewRows + (f.g.n_groups < f.g.M ? f.g.n_groups : f.g.M) + 1;
-    return launch<T, XT, MxRows, 64, 4>(f, units, st);
+    if (units * ((f.g.N + 31) / 32) < 256) return launch<T, XT, MxRows, 16, 4>(f, units, st);
+    return launch<T, XT, MxRows, 32, 4>(f, units, st);
 }
 
 bool mx_few_fits(int64_t M, int64_t kp) {

