@@ -197,15 +197,14 @@ bool mx_few_fits(int64_t M, int64_t kp) {
     return few_lds(kp, M < kFewRows ? M : kFewRows, 8) <= kMxMaxLds;
 }
 
-int mx_few_packed(const MxFArgs& f, int c_dtype, hipStream_t st) {
-    return c_dtype == NVFP4_BF16 ? launch_dense<uint16_t, uint8_t>(f, st) : launch_dense<float, uint8_t>(f, st);
-}
-
 template <typename XT>
 static int launch_x(const MxFArgs& f, int c_dtype, hipStream_t st) {
     if (f.g.n_groups) return c_dtype == NVFP4_BF16 ? launch_rows<uint16_t, XT>(f, st) : launch_rows<float, XT>(f, st);
     return c_dtype == NVFP4_BF16 ? launch_dense<uint16_t, XT>(f, st) : launch_dense<float, XT>(f, st);
 }
+
+int mx_few_packed(const MxFArgs& f, int c_dtype, hipStream_t st) { return launch_x<uint8_t>(f, c_dtype, st); }
+
 int mx_few_linear(const MxFArgs& f, int x_dtype, int c_dtype, hipStream_t st) {
     return x_dtype == NVFP4_BF16 ? launch_x<uint16_t>(f, c_dtype, st) : launch_x<float>(f, c_dtype, st);
 }

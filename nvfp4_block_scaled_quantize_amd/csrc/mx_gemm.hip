@@ -79,6 +79,12 @@ extern "C" int mxfp4_gemm_grouped(const mxfp4_tensor* a, const mxfp4_tensor* b, 
     if (empty) return NVFP4_OK;
     const MxGArgs g = {a->codes, a->scales, b->codes, b->scales, M, N, mx_pad(K), 0, c, ldc,
                        offsets, (int)n_groups};
+    const int64_t busy = n_groups < M ? n_groups : M;
+    // Up to 16 Ki elements of A a group, or a row, go to the kernel that streams B once (4096 x 2048,
+    // 17 groups: 80 rows 16.7 us against 19.8, 136 rows 18.2 against 19.9, 280 rows 20.8 against
+    // 20.1; 2048 x 6144, 8 groups: 16 rows 12.5 against 15.3, 96 rows 17.5 against 15.4).
+    if (M * g.kp <= busy * (g.kp > 16384 ? g.kp : 16384) && mx_few_fits(M, g.kp))
+        return mx_few_packed({g, nullptr, 0, K, 0}, c_dtype, (hipStream_t)stream);
     return launch_gemm<MxRows>(g, c_dtype, (hipStream_t)stream);
 }
 
@@ -105,9 +111,9 @@ static size_t linear_code_bytes(int64_t M, int64_t K) {
 // 16 x 4096 x 2048 (32 Ki elements, one round) 6.1 us of GPU time against 6.5 as two kernels, 12 x
 // 4096 x 4096 (48 Ki) 8.2 against 7.6, but 8.1 against 9.9 by the host's clock; 8 x 1024 x 8192 (64
 // Ki) 10.9 against 8.7, 16 x 9216 x 2048 (32 Ki, 2.25 rounds) 11.6 against 8.4.  Grouped: up to 8 Ki elements, or a row, a group.  Of N x K
-// 4096 x 2048 and 17 groups 40 rows (5 Ki a group) 17.4 against 22.7, 60 rows 19.6 against 22.7; of
-// 1536 x 2048 and 29 groups 64 rows 14.2 against 15.9, 128 rows (9 Ki) 20.5 against 15.9; of 9216 x
-// 4096 and 4 groups 8 rows 17.1 against 22.1, 16 rows (16 Ki) 24.4 against 22.1.
+// 4096 x 2048 and 17 groups 40 rows (5 Ki a group) 17.4 against 19.5, 60 rows 19.6 against 19.9; of
+// 1536 x 2048 and 29 groups 64 rows 14.3 against 14.8, 128 rows (9 Ki) 20.5 against 15.1; of 9216 x
+// 4096 and 4 groups 8 rows 17.1 against 19.3, 16 rows (16 Ki) 24.4 against 22.9.
 static bool linear_fused(int64_t M, int64_t N, int64_t K, int64_t n_groups) {
     const int64_t kp = mx_pad(K), busy = n_groups < M ? n_groups : M, tiles = (N + 15) / 16;
     if (M <= 0 || K <= 0 || !mx_few_fits(M, kp)) return false;
