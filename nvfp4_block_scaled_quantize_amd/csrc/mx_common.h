@@ -306,19 +306,21 @@ struct MxGArgs {
     int n_groups;
 };
 
-// A product with few rows (mx_few.hip): A packed (x null), or x to quantize rowwise.
+// A product for mx_few.hip: A packed (x null), or x to quantize rowwise.
 struct MxFArgs {
     MxGArgs g;
     const void* x;
     int64_t ldx, K;
     uint32_t above;
 };
-// A packed with at most 16 rows, not grouped.
+// A packed, dense or grouped.
 int mx_few_packed(const MxFArgs& f, int c_dtype, hipStream_t st);
-// x: at most 16 rows, or grouped (in units of 16 rows of a group).
+// x: at most 16 rows, or grouped.
 int mx_few_linear(const MxFArgs& f, int x_dtype, int c_dtype, hipStream_t st);
-// Whether a workgroup's rows of A fit into LDS.
+// Whether 16 rows of A fit into a workgroup's LDS, and whether a dense product of A packed belongs
+// here: up to 16 rows, or no more than two workgroups (of 32 x 32) a compute unit.
 bool mx_few_fits(int64_t M, int64_t kp);
+bool mx_few_dense(int64_t M, int64_t N, int64_t kp);
 
 constexpr int kMxMaxLds = 160 * 1024;
 // Lets a kernel use `bytes` of LDS, once per device (a bit of `ready` each).

@@ -64,8 +64,11 @@ extern "C" int mxfp4_gemm(const mxfp4_tensor* a, const mxfp4_tensor* b, int64_t 
     if (int rc = check_gemm(a, b, M, N, K, c, c_dtype, ldc, &empty)) return rc;
     if (empty) return NVFP4_OK;
     const MxGArgs g = {a->codes, a->scales, b->codes, b->scales, M, N, mx_pad(K), 0, c, ldc, nullptr, 0};
-    // Up to 16 rows go to the kernel that streams B once (16 x 6144 x 4096 6.6 us against 10.2).
-    if (M <= 16 && mx_few_fits(M, g.kp)) return mx_few_packed({g, nullptr, 0, K, 0}, c_dtype, (hipStream_t)stream);
+    // Few rows, and products of few tiles, go to the kernel that splits K over the waves of a
+    // workgroup: 16 x 6144 x 4096 6.1 us against 10.7, 77 x 4999 x 2056 (471 of its workgroups) 6.0
+    // against 8.9, 256 x 1024 x 4096 (256) 5.8 against 10.7; but 64 x 9216 x 2048 (576) 7.8 either way,
+    // 128 x 6144 x 4096 (768) 12.8 against 11.5.
+    if (mx_few_dense(M, N, g.kp)) return mx_few_packed({g, nullptr, 0, K, 0}, c_dtype, (hipStream_t)stream);
     return launch_gemm<MxDense>(g, c_dtype, (hipStream_t)stream);
 }
 
@@ -80,10 +83,11 @@ extern "C" int mxfp4_gemm_grouped(const mxfp4_tensor* a, const mxfp4_tensor* b, 
     const MxGArgs g = {a->codes, a->scales, b->codes, b->scales, M, N, mx_pad(K), 0, c, ldc,
                        offsets, (int)n_groups};
     const int64_t busy = n_groups < M ? n_groups : M;
-    // Up to 16 Ki elements of A a group, or a row, go to the kernel that streams B once (4096 x 2048,
-    // 17 groups: 80 rows 16.7 us against 19.8, 136 rows 18.2 against 19.9, 280 rows 20.8 against
-    // 20.1; 2048 x 6144, 8 groups: 16 rows 12.5 against 15.3, 96 rows 17.5 against 15.4).
-    if (M * g.kp <= busy * (g.kp > 16384 ? g.kp : 16384) && mx_few_fits(M, g.kp))
+    // Up to 48 Ki elements of A a group, or a row, go to the kernel that streams B (4096 x 2048, 17
+    // groups: 80 rows 14.2 us against 19.8, 400 rows 17.8 against 20.2; 2048 x 6144, 8 groups: 16 rows
+    // 11.4 against 15.0; 9216 x 4096, 4 groups: 32 rows 17.3 against 19.3, 64 rows (64 Ki a group)
+    // 21.2 against 19.5).
+    if (M * g.kp <= busy * (g.kp > 48 << 10 ? g.kp : 48 << 10) && mx_few_fits(M, g.kp))
         return mx_few_packed({g, nullptr, 0, K, 0}, c_dtype, (hipStream_t)stream);
     return launch_gemm<MxRows>(g, c_dtype, (hipStream_t)stream);
 }
@@ -107,13 +111,13 @@ static size_t linear_code_bytes(int64_t M, int64_t K) {
 }
 
 // Few rows are quantized inside the product, which saves a launch (about 3 us) and the workspace,
-// as long as every workgroup's doing so costs less.  Dense: elements times rounds of workgroups.
-// 16 x 4096 x 2048 (32 Ki elements, one round) 6.1 us of GPU time against 6.5 as two kernels, 12 x
-// 4096 x 4096 (48 Ki) 8.2 against 7.6, but 8.1 against 9.9 by the host's clock; 8 x 1024 x 8192 (64
-// Ki) 10.9 against 8.7, 16 x 9216 x 2048 (32 Ki, 2.25 rounds) 11.6 against 8.4.  Grouped: up to 8 Ki elements, or a row, a group.  Of N x K
-// 4096 x 2048 and 17 groups 40 rows (5 Ki a group) 17.4 against 19.5, 60 rows 19.6 against 19.9; of
-// 1536 x 2048 and 29 groups 64 rows 14.3 against 14.8, 128 rows (9 Ki) 20.5 against 15.1; of 9216 x
-// 4096 and 4 groups 8 rows 17.1 against 19.3, 16 rows (16 Ki) 24.4 against 22.9.
+// as long as every workgroup's doing so costs less.  Dense: elements times rounds of workgroups, up
+// to 48 Ki.  16 x 4096 x 2048 (32 Ki, one round) 5.6 us of GPU time against 6.3 as two kernels, 12 x
+// 4096 x 4096 (48 Ki) 7.0 against 6.9 and a launch less; 8 x 1024 x 8192 (64 Ki) 9.1 against 7.8, 16 x
+// 9216 x 2048 (32 Ki, 2.25 rounds) 9.9 against 7.5.  Grouped: up to 8 Ki elements, or a row, a group.
+// Of N x K 4096 x 2048 and 17 groups 40 rows (5 Ki a group) 16.2 against 17.0, 60 rows (7 Ki) 18.0
+// against 17.3; of 1536 x 2048 and 29 groups 64 rows 12.0 against 13.3, 128 rows (9 Ki) 15.4 against
+// 14.2; of 9216 x 4096 and 4 groups 8 rows 16.0 against 18.2, 16 rows (16 Ki) 21.4 against 19.4.
 static bool linear_fused(int64_t M, int64_t N, int64_t K, int64_t n_groups) {
     const int64_t kp = mx_pad(K), busy = n_groups < M ? n_groups : M, tiles = (N + 15) / 16;
     if (M <= 0 || K <= 0 || !mx_few_fits(M, kp)) return false;

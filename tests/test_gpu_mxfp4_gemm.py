@@ -253,6 +253,45 @@ def test_few_rows(nv, case):
                 assert (c[~inside] == 0).all()
 
 
+# the few-row kernel's other tiles: (M, N, K, offsets)
+SMALL = [(20, 2000, 512, None), (24, 4000, 256, None), (130, 3000, 96, None), (40, 33, 9000, None), (40, 33, 10000, None),
+         (100, 1500, 10000, None), (1000, 250, 1030, None), (8000, 30, 100, None),
+         (200, 130, 300, [0, 100, 100, 101, 133, 133, 190, 196, 197]), (90, 600, 2100, [3, 40, 90])]
+
+
+@pytest.mark.parametrize("case", range(len(SMALL)))
+def test_small_products(nv, case):
+    M, N, K, off = SMALL[case]
+    print(f"small {case}", flush=True)
+    a, b = copy_of(nv, (M,), K, 41), copy_of(nv, (N,) if off is None else (len(off) - 1, N), K, 42)
+    av, bv = values(a), values(b)
+    for dt, name in DTYPES:
+        if off is None:
+            check(nv.mxfp4_gemm(a, b, out_dtype=dt), *product(av, bv), f"small {name}")
+            continue
+        c = nv.mxfp4_gemm_grouped(a, b, torch.tensor(off, dtype=torch.int32, device=dev()), out_dtype=dt)
+        inside = torch.zeros(M, dtype=torch.bool, device=dev())
+        for g, (i, j) in enumerate(ref.spans(off, M)):
+            inside[i:j] = True
+            if j > i:
+                check(c[i:j], *product(av[i:j], bv[g]), f"small {name}")
+        assert (c[~inside] == 0).all()
+
+
+def test_nan_blocks_stay_in_their_rows_and_columns(nv):
+    """A NaN block makes its row of C, and only that, NaN; whatever tile the product takes."""
+    for M, N, K in [(16, 40, 700), (24, 4000, 300), (64, 300, 2080), (700, 600, 300), (2304, 2560, 320)]:
+        a, b = copy_of(nv, (M,), K, 43), copy_of(nv, (N,), K, 44)
+        a.scales[M - 3, 1], b.scales[5, -(-K // 32) - 1] = 255, 255
+        want, absdot = product(torch.nan_to_num(values(a)), torch.nan_to_num(values(b)))
+        c = nv.mxfp4_gemm(a, b)
+        nan = torch.zeros(M, N, dtype=torch.bool, device=dev())
+        nan[M - 3], nan[:, 5] = True, True
+        assert torch.equal(torch.isnan(c), nan)
+        keep = ~nan
+        check(c[keep], want[keep], absdot[keep], "beside NaN")
+
+
 def test_large_tiles_with_one_row_and_short_k(nv):
     """Tiles of one row or column, K of less than a stage, groups of no and of one row of K."""
     for M, N, K in [(4097, 4096, 30), (4096, 4097, 130), (4097, 4097, 1)]:
