@@ -15,9 +15,11 @@ namespace nvfp4 {
 // 4096 x 2048 the same).  float32 does where C is larger than the last-level cache (256 MB), so
 // that no reader could find much of it there: 15 gradients of 4096 x 2048 (503 MB) 109 us against
 // 141, 8192 x 9216 x 4096 (302 MB) with its reader 227 against 242; but 268 MB (8192 x 8192 x 2048)
-// with a reader 157 against 145, 134 MB 109 against 100.
+// with a reader 157 against 145, 134 MB 109 against 100.  Gradients of groups are read after the
+// whole backward pass: they do from half of that on, which leaves the cache to the next layer's
+// operands (15 of 1536 x 2048, 189 MB: 43 us either way, a step of their layer 164 against 187).
 static bool streams(const MxGArgs& g, int mode) {
-    return g.M * g.N * 4 * (mode == MxK ? g.n_groups : 1) > ((int64_t)256 << 20);
+    return mode == MxK ? g.M * g.N * 4 * g.n_groups > ((int64_t)128 << 20) : g.M * g.N * 4 > ((int64_t)256 << 20);
 }
 
 // Which tile.  256 x 256 tiles run one to a compute unit, 256 at a time; 128 x 128 tiles two to a
