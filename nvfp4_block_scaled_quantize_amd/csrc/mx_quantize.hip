@@ -54,7 +54,9 @@ __device__ __forceinline__ uint32_t codes_of(const Oct<T>& o, uint32_t code, boo
 
 // Rowwise copy alone: a lane per eight elements, a quad per block, so that loads and stores
 // are contiguous over the wave.  A workgroup takes kRowSteps times 256 consecutive octs of the
-// copy (rows padded to row_kp), all loaded before the first is used.
+// copy (rows padded to row_kp), all loaded before the first is used.  From memory (inputs of 600 MB
+// in turn) 8192 x 9216 bfloat16 37 us, 5.2 TB/s read and written; 16 x 4096 2.7 us, an empty kernel's
+// time.
 constexpr int kRowSteps = 4;
 template <typename T, bool SR>
 __global__ __launch_bounds__(256) void k_mx_rows(MxQArgs g) {
@@ -88,7 +90,8 @@ __global__ __launch_bounds__(256) void k_mx_rows(MxQArgs g) {
 // registers, and put into LDS as dwords [row][64]; then a thread takes one dword column (two
 // bfloat16 columns or one float32 one) of 32 rows.  Dword c of row r lies at c ^ 16 (r / 32), so
 // that the four row blocks of 16 dword columns, which a wave reads at once (a quad of lanes
-// per column, for 64 contiguous bytes of its codes), are in different banks.
+// per column, for 64 contiguous bytes of its codes), are in different banks.  From memory 8192 x 9216
+// bfloat16 49 us, 4.7 TB/s; 8192 x 4608 float32 47 us, 4.0 TB/s.
 template <typename T, bool SR>
 __global__ __launch_bounds__(256) void k_mx_tile(MxQArgs g, unsigned units, unsigned col_tiles) {
     constexpr int kTileCols = 256 / sizeof(T), kPerRow = kTileCols / 8;   // octs of a tile row
