@@ -313,14 +313,15 @@ struct MxFArgs {
     int64_t ldx, K;
     uint32_t above;
 };
-// A packed, dense or grouped.
+// A packed, or quantized from x; dense or grouped.
 int mx_few_packed(const MxFArgs& f, int c_dtype, hipStream_t st);
-// x: at most 16 rows, or grouped.
 int mx_few_linear(const MxFArgs& f, int x_dtype, int c_dtype, hipStream_t st);
 // Whether 16 rows of A fit into a workgroup's LDS, and whether a dense product of A packed belongs
 // here: up to 16 rows, or no more than two workgroups (of 32 x 32) a compute unit.
 bool mx_few_fits(int64_t M, int64_t kp);
 bool mx_few_dense(int64_t M, int64_t N, int64_t kp);
+// Elements of x that a workgroup of a dense product quantizes, times the workgroups a compute unit.
+int64_t mx_few_quantized(int64_t M, int64_t N, int64_t kp);
 
 constexpr int kMxMaxLds = 160 * 1024;
 // Lets a kernel use `bytes` of LDS, once per device (a bit of `ready` each).

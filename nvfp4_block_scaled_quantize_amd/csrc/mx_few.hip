@@ -235,23 +235,29 @@ static int launch(const MxFArgs& f, int64_t units, hipStream_t st) {
     return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
 }
 
-// Dense, up to 16 rows: 16 columns a workgroup.  Eight waves halve a wave's K (1 x 1024 x 8192 4.6
-// against 5.0 us, 16 x 6144 x 4096 6.1 against 6.3), but with more than about 448 workgroups four
-// are enough and start sooner (1 x 16384 x 2048 5.3 against 6.5 us, 4 x 9216 x 2048 4.9 against 5.2).
-// More rows (packed): the smallest tile that leaves no compute unit two workgroups, or else 32 x 32.
-// 32 x 1024 x 4096: 16 x 16 4.0 us, 32 x 16 4.5; 128 x 1024 x 4096: 5.5, 4.7, 32 x 32 5.7; 64 x 6144 x
-// 4096: 13.0, 9.4, 9.1.
+// The tile of a dense product.  Up to 16 rows: 16 columns a workgroup.  Eight waves halve a wave's K
+// (1 x 1024 x 8192 4.6 against 5.0 us, 16 x 6144 x 4096 6.1 against 6.3), but with more than about 448
+// workgroups four are enough and start sooner (1 x 16384 x 2048 5.3 against 6.5 us, 4 x 9216 x 2048
+// 4.9 against 5.2).  More rows: the smallest tile that leaves no compute unit two workgroups, or else
+// 32 x 32.  Packed, 32 x 1024 x 4096: 16 x 16 4.0 us, 32 x 16 4.5; 128 x 1024 x 4096: 5.5, 4.7, 32 x 32
+// 5.7; 64 x 6144 x 4096: 13.0, 9.4, 9.1.
+struct FewTile {
+    int blocks, cols;
+    int64_t units, workgroups;
+};
+static FewTile few_tile(int64_t M, int64_t N) {
+    const int64_t units = (M + 15) / 16, pairs = (M + 31) / 32, tn = (N + 15) / 16;
+    if (units == 1 || units * tn <= 256) return {1, 16, units, units * tn};
+    if (pairs * tn <= 256) return {2, 16, pairs, pairs * tn};
+    return {2, 32, pairs, pairs * ((N + 31) / 32)};
+}
 template <typename T, typename XT>
 static int launch_dense(const MxFArgs& f, hipStream_t st) {
-    const int64_t tn = (f.g.N + 15) / 16, units = (f.g.M + 15) / 16, pairs = (units + 1) / 2;
-    if constexpr (sizeof(XT) == 1) {
-        if (units > 1 && few_fits(f.g.kp, f.g.M, 2)) {
-            if (units * tn > 256 && pairs * tn <= 256) return launch<T, XT, MxDense, 16, 8, 2>(f, pairs, st);
-            if (units * tn > 256) return launch<T, XT, MxDense, 32, 8, 2>(f, pairs, st);
-        }
-    }
-    if (units * tn > 448) return launch<T, XT, MxDense, 16, 4>(f, units, st);
-    return launch<T, XT, MxDense, 16, 8>(f, units, st);
+    const FewTile t = few_tile(f.g.M, f.g.N);
+    if (t.cols == 32) return launch<T, XT, MxDense, 32, 8, 2>(f, t.units, st);
+    if (t.blocks == 2) return launch<T, XT, MxDense, 16, 8, 2>(f, t.units, st);
+    if (t.workgroups > 448) return launch<T, XT, MxDense, 16, 4>(f, t.units, st);
+    return launch<T, XT, MxDense, 16, 8>(f, t.units, st);
 }
 
 // Grouped: four waves on 16 rows and 32 columns, two of them sharing K (80 packed rows over 17
@@ -273,8 +279,14 @@ static int launch_rows(const MxFArgs& f, hipStream_t st) {
 bool mx_few_fits(int64_t M, int64_t kp) { return few_fits(kp, M, 1); }
 
 bool mx_few_dense(int64_t M, int64_t N, int64_t kp) {
-    if (M > 16 && (M + 31) / 32 * ((N + 31) / 32) > 512) return false;
-    return few_fits(kp, M, M > 16 && (M + 15) / 16 * ((N + 15) / 16) > 256 ? 2 : 1);
+    const FewTile t = few_tile(M, N);
+    return (M <= 16 || t.workgroups <= 512) && few_fits(kp, M, t.blocks);
+}
+
+int64_t mx_few_quantized(int64_t M, int64_t N, int64_t kp) {
+    const FewTile t = few_tile(M, N);
+    const int64_t rows = M < kFewRows * t.blocks ? M : kFewRows * t.blocks;
+    return rows * kp * (t.workgroups > 256 ? t.workgroups : 256) / 256;
 }
 
 template <typename XT>

@@ -113,18 +113,21 @@ static size_t linear_code_bytes(int64_t M, int64_t K) {
 }
 
 // Few rows are quantized inside the product, which saves a launch (about 3 us) and the workspace,
-// as long as every workgroup's doing so costs less.  Dense: elements times rounds of workgroups, up
-// to 48 Ki.  16 x 4096 x 2048 (32 Ki, one round) 5.6 us of GPU time against 6.3 as two kernels, 12 x
-// 4096 x 4096 (48 Ki) 7.0 against 6.9 and a launch less; 8 x 1024 x 8192 (64 Ki) 9.1 against 7.8, 16 x
-// 9216 x 2048 (32 Ki, 2.25 rounds) 9.9 against 7.5.  Grouped: up to 8 Ki elements, or a row, a group.
-// Of N x K 4096 x 2048 and 17 groups 40 rows (5 Ki a group) 16.2 against 17.0, 60 rows (7 Ki) 18.0
-// against 17.3; of 1536 x 2048 and 29 groups 64 rows 12.0 against 13.3, 128 rows (9 Ki) 15.4 against
-// 14.2; of 9216 x 4096 and 4 groups 8 rows 16.0 against 18.2, 16 rows (16 Ki) 21.4 against 19.4.
+// as long as every workgroup's doing so costs less.  Dense: a workgroup's elements times the
+// workgroups a compute unit, up to 48 Ki.  64 x 1024 x 2048 (32 Ki) 5.6 us of GPU time against 6.4 as
+// two kernels, 32 x 4096 x 1024 (32 Ki) 6.0 against 6.5, 12 x 4096 x 4096 (48 Ki) 7.0
+// against 6.9 and a launch less; 32 x 1024 x 4096 (64 Ki) 8.2 against 7.0, 16 x 9216 x 2048 (72 Ki)
+// 10.0 against 7.6.  One or two rows cost less than the launch whatever their length: 1 x 50000 x
+// 4096 20.2 against 23.2, 2 x 21.5 against 23.3, 4 x 26.4 against 23.7.  Grouped: up to 8 Ki elements,
+// or a row, a group.  Of N x K 4096 x 2048 and 17 groups 40 rows (5 Ki a group) 16.2 against 17.0, 60
+// rows (7 Ki) 18.0 against 17.3; of 1536 x 2048 and 29 groups 64 rows 12.0 against 13.3, 128 rows (9
+// Ki) 15.4 against 14.2; of 9216 x 4096 and 4 groups 8 rows 16.0 against 18.2, 16 rows (16 Ki) 21.4
+// against 19.4.
 static bool linear_fused(int64_t M, int64_t N, int64_t K, int64_t n_groups) {
-    const int64_t kp = mx_pad(K), busy = n_groups < M ? n_groups : M, tiles = (N + 15) / 16;
-    if (M <= 0 || K <= 0 || !mx_few_fits(M, kp)) return false;
-    if (n_groups) return M * kp <= busy * (kp > 8192 ? kp : 8192);
-    return M <= 16 && M * kp <= (48 << 10) * 256 / (tiles > 256 ? tiles : 256);
+    const int64_t kp = mx_pad(K), busy = n_groups < M ? n_groups : M;
+    if (M <= 0 || K <= 0) return false;
+    if (n_groups) return M * kp <= busy * (kp > 8192 ? kp : 8192) && mx_few_fits(M, kp);
+    return mx_few_dense(M, N, kp) && (M <= 2 || mx_few_quantized(M, N, kp) <= 48 << 10);
 }
 
 extern "C" size_t mxfp4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t n_groups) {

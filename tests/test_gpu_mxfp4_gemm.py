@@ -278,6 +278,21 @@ def test_small_products(nv, case):
         assert (c[~inside] == 0).all()
 
 
+@pytest.mark.parametrize("M,N,K", [(17, 100, 300), (32, 1024, 1000), (40, 1000, 96), (64, 1024, 1030), (100, 2100, 130),
+                                   (250, 1000, 513), (1000, 500, 64), (33, 4500, 520), (2, 9000, 1000), (5, 9000, 3000)])
+def test_small_linear(nv, M, N, K):
+    """The quantization inside the product at every tile of it, and as its own kernel beyond."""
+    print(f"small linear {M}x{N}x{K}", flush=True)
+    for dtype in (torch.bfloat16, torch.float32):
+        x = torch.randn(M, K + 3, device=dev()).to(dtype)[:, 1:1 + K]
+        w = copy_of(nv, (N,), K, 45)
+        for rule in (ref.FLOOR, ref.CEIL):
+            q = nv.mxfp4_quantize(x, nv.mxfp4_quant_params(scale_rule=rule))[0]
+            want, absdot = product(values(q), values(w))
+            for dt, name in DTYPES:
+                check(nv.mxfp4_linear(x, w, scale_rule=rule, out_dtype=dt), want, absdot, f"linear {name}")
+
+
 def test_nan_blocks_stay_in_their_rows_and_columns(nv):
     """A NaN block makes its row of C, and only that, NaN; whatever tile the product takes."""
     for M, N, K in [(16, 40, 700), (24, 4000, 300), (64, 300, 2080), (700, 600, 300), (2304, 2560, 320)]:
@@ -362,8 +377,9 @@ def test_linear_on_another_stream_and_in_a_graph(nv):
     x = torch.randn(33, 640, device=dev()).bfloat16()
     w = copy_of(nv, (700,), 640, 9)
     off = torch.tensor([0, 10, 33], dtype=torch.int32, device=dev())
-    ws = torch.empty(nv.mxfp4_linear_workspace_bytes(33, 700, 640), dtype=torch.uint8, device=dev())
     w2 = copy_of(nv, (2, 300), 640, 10)
+    need = max(nv.mxfp4_linear_workspace_bytes(33, 700, 640), nv.mxfp4_linear_workspace_bytes(33, 300, 640, 2))
+    ws = torch.empty(need, dtype=torch.uint8, device=dev())
     big, bigw = copy_of(nv, (600,), 640, 11), copy_of(nv, (512,), 640, 12)
     eager = [nv.mxfp4_linear(x, w), nv.mxfp4_linear(x, w2, offsets=off), nv.mxfp4_gemm(big, bigw)]
     side = torch.cuda.Stream()
@@ -425,7 +441,7 @@ def test_refusals(nv):
            lambda: nv.mxfp4_linear(x, e(8, 63)), lambda: nv.mxfp4_linear(x, e((1, 8), 64)),
            lambda: nv.mxfp4_linear(x, e((2, 8), 64), offsets=off), lambda: nv.mxfp4_linear(x.half(), e(8, 64)),
            lambda: nv.mxfp4_linear(x, e(8, 64), scale_rule=2),
-           lambda: nv.mxfp4_linear(x.t(), e(8, 8)), lambda: nv.mxfp4_linear(x.repeat(9, 1), e(8, 64), workspace=torch.empty(1, dtype=torch.uint8, device=d)),
+           lambda: nv.mxfp4_linear(x.t(), e(8, 8)), lambda: nv.mxfp4_linear(x.repeat(2200, 1), e(8, 64), workspace=torch.empty(1, dtype=torch.uint8, device=d)),
            lambda: nv.mxfp4_gemm(nv.MXTensor(e(8, 64).codes[:, ::2], e(8, 64).scales, 64), e(8, 64)),
            lambda: nv.mxfp4_gemm(nv.MXTensor(e(8, 64).codes.cpu(), e(8, 64).scales, 64), e(8, 64))]
     for i, f in enumerate(bad):

@@ -91,12 +91,12 @@ def test_product_argument_errors(nv):
     assert r(o=None) == -1 and r(n=0) == -2 and r(n=-1) == -2 and r(M=1 << 31) == -2 and r(M=0) == 0
     w = lambda o=off, n=2, rows=8, M=8: lib.mxfp4_gemm_grouped_wgrad(a, b, o, n, M, 8, rows, c, 0, 8, None)
     assert w(o=None) == -1 and w(n=0) == -2 and w(rows=-1) == -2 and w(rows=1 << 24) == -2 and w(M=0) == 0
-    need = lib.mxfp4_linear_workspace_bytes(64, 8, 8, 0)
-    ln = lambda ws=FAKE + 0x60000, size=1 << 20, rule=0, K=8, ld=8, x=FAKE, N=8, o=None, n=0, dt=1, M=64: \
+    need = lib.mxfp4_linear_workspace_bytes(17000, 8, 8, 0)
+    ln = lambda ws=FAKE + 0x60000, size=1 << 21, rule=0, K=8, ld=8, x=FAKE, N=8, o=None, n=0, dt=1, M=17000: \
         lib.mxfp4_linear(x, dt, M, K, ld, rule, b, N, o, n, c, 0, 8, ws, size, None)
     assert need > 0 and ln(size=need - 1) == -6 and ln(ws=None) == -6
     assert lib.mxfp4_linear_workspace_bytes(1, 8, 8, 0) == 0     # quantized inside the product
-    for m in (64, 1):
+    for m in (17000, 1):
         assert ln(M=m, ws=FAKE + 16) == -3 and ln(M=m, rule=2) == -5 and ln(M=m, ld=7) == -2
         assert ln(M=m, K=-1) == -2 and ln(M=m, N=-1) == -2 and ln(M=m, x=None) == -1
         assert ln(M=m, dt=3) == -4 and ln(M=m, n=2) == -1 and ln(M=m, o=off) == -5
