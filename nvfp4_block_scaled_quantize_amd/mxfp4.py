@@ -80,14 +80,21 @@ def _lib():
     return _bound
 
 
-def _check(rc):
-    if rc != 0:
-        raise _error(f"nvfp4 status {rc}: {_lib().nvfp4_status_string(rc).decode()}")
-
-
 # The current stream's handle by device index: a call of these operators can be shorter than
 # building the torch.cuda.Stream object that would otherwise carry it (0.1 against 1.9 us).
 _stream = torch._C._cuda_getCurrentRawStream
+_current = torch._C._cuda_getDevice
+
+
+def _call(f, device, *args):
+    """f(*args, stream) on the tensors' device, which need not be the current one."""
+    if _current() == device:
+        rc = f(*args, _stream(device))
+    else:
+        with torch.cuda.device(device):
+            rc = f(*args, _stream(device))
+    if rc != 0:
+        raise _error(f"nvfp4 status {rc}: {_lib().nvfp4_status_string(rc).decode()}")
 
 
 @dataclass
@@ -246,9 +253,8 @@ def mxfp4_quantize(x, params, offsets=None, row_out=None, col_out=None):
             cc, got = _operand(col, "col_out", dev)
             if got[:-1] != (*lead, C) or col.k != R or col.n_groups != groups:
                 raise _error(f"col_out {col.shape} does not hold x {tuple(shape)} transposed")
-    _check(_lib().mxfp4_quantize(x.data_ptr(), dtype, batch, R, C, pitch,
-                                 x.stride(0) if batch > 1 else 0, op, groups, params, rc, cc,
-                                 _stream(dev)))
+    _call(_lib().mxfp4_quantize, dev, x.data_ptr(), dtype, batch, R, C, pitch,
+          x.stride(0) if batch > 1 else 0, op, groups, params, rc, cc)
     return row, col
 
 
@@ -266,7 +272,7 @@ def mxfp4_dequantize(q, out_dtype=torch.float32, offsets=None, out=None):
             raise _error("out of a stack of matrices must be contiguous")
         for d in shape[1:-1]:
             n *= d
-    _check(_lib().mxfp4_dequantize(qc, n, q.k, op, groups, dtype, out.data_ptr(), pitch, _stream(dev)))
+    _call(_lib().mxfp4_dequantize, dev, qc, n, q.k, op, groups, dtype, out.data_ptr(), pitch)
     return out
 
 
@@ -281,7 +287,7 @@ def mxfp4_gemm(a, b, out=None, out_dtype=torch.float32):
         raise _error(f"K mismatch {a.k} vs {b.k}")
     M, N = sa[0], sb[0]
     out, dtype, pitch = _output(out, (M, N), out_dtype, a.codes)
-    _check(_lib().mxfp4_gemm(ac, bc, M, N, a.k, out.data_ptr(), dtype, pitch, _stream(dev)))
+    _call(_lib().mxfp4_gemm, dev, ac, bc, M, N, a.k, out.data_ptr(), dtype, pitch)
     return out
 
 
@@ -300,8 +306,7 @@ def mxfp4_gemm_grouped(a, b, offsets, out=None, out_dtype=torch.float32):
         raise _error(f"K mismatch {a.k} vs {b.k}")
     M, N = sa[0], sb[1]
     out, dtype, pitch = _output(out, (M, N), out_dtype, a.codes)
-    _check(_lib().mxfp4_gemm_grouped(ac, bc, op, groups, M, N, a.k, out.data_ptr(), dtype, pitch,
-                                     _stream(dev)))
+    _call(_lib().mxfp4_gemm_grouped, dev, ac, bc, op, groups, M, N, a.k, out.data_ptr(), dtype, pitch)
     return out
 
 
@@ -320,8 +325,7 @@ def mxfp4_gemm_grouped_wgrad(a, b, offsets, out=None, out_dtype=torch.float32):
     out, dtype, _ = _output(out, (groups, M, N), out_dtype, a.codes)
     if not out.is_contiguous():
         raise _error("out must be contiguous")
-    _check(_lib().mxfp4_gemm_grouped_wgrad(ac, bc, op, groups, M, N, a.k, out.data_ptr(), dtype, N,
-                                           _stream(dev)))
+    _call(_lib().mxfp4_gemm_grouped_wgrad, dev, ac, bc, op, groups, M, N, a.k, out.data_ptr(), dtype, N)
     return out
 
 
@@ -352,6 +356,6 @@ def mxfp4_linear(x, w, offsets=None, scale_rule=MXFP4_SCALE_FLOOR, out=None, out
     elif workspace.get_device() != dev or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise _error("workspace must be a contiguous uint8 tensor on x's device")
     ws, ws_bytes = (workspace.data_ptr(), workspace.numel()) if workspace is not None else (None, 0)
-    _check(lib.mxfp4_linear(x.data_ptr(), xdtype, M, K, xpitch, scale_rule, wc, N, op, groups,
-                            out.data_ptr(), dtype, pitch, ws, ws_bytes, _stream(dev)))
+    _call(lib.mxfp4_linear, dev, x.data_ptr(), xdtype, M, K, xpitch, scale_rule, wc, N, op, groups,
+          out.data_ptr(), dtype, pitch, ws, ws_bytes)
     return out

@@ -137,3 +137,25 @@ def test_reference_rounding_by_hand():
     assert ref.quantize_rows(np.full((1, 32), 7.0), ref.CEIL)[1][0, 0] == 128
     assert ref.quantize_rows(np.full((1, 32), 6.0), ref.CEIL)[1][0, 0] == 127
     assert ref.quantize_rows(np.full((1, 32), np.inf))[1][0, 0] == 255
+
+
+def test_calls_run_on_their_tensors_device(monkeypatch):
+    """A call whose tensors are on another device than the current one switches to it for the call."""
+    import contextlib
+    from nvfp4_block_scaled_quantize_amd import mxfp4
+    entered = []
+
+    @contextlib.contextmanager
+    def device(d):
+        entered.append(d)
+        yield
+        entered.append("left")
+
+    monkeypatch.setattr(mxfp4, "_current", lambda: 0)
+    monkeypatch.setattr(mxfp4, "_stream", lambda d: 100 + d)
+    monkeypatch.setattr(mxfp4.torch.cuda, "device", device)
+    seen = []
+    f = lambda *a: seen.append((list(entered), a)) or 0
+    mxfp4._call(f, 0, 5)
+    mxfp4._call(f, 1, 6)
+    assert seen == [([], (5, 100)), ([1], (6, 101))] and entered == [1, "left"]
