@@ -16,7 +16,7 @@ only marshals arguments; there is no CPU path.
 holds rows offsets[g] .. offsets[g+1].  It stays on the device; no call reads it on the host.
 """
 import ctypes
-from dataclasses import dataclass
+import math
 
 import torch
 
@@ -97,30 +97,66 @@ def _call(f, device, *args):
         raise _error(f"nvfp4 status {rc}: {_lib().nvfp4_status_string(rc).decode()}")
 
 
-@dataclass
 class MXTensor:
     """One copy on the GPU: codes uint8 [..., n, kp/2], scales uint8 [..., n, kp/32], where kp
     is k rounded up to a multiple of 128, or, for a grouped columnwise copy (n_groups > 0, k
-    the number of grouped rows), mxfp4_grouped_k(k, n_groups)."""
-    codes: torch.Tensor
-    scales: torch.Tensor
-    k: int
-    n_groups: int = 0
+    the number of grouped rows), mxfp4_grouped_k(k, n_groups).
 
-    @property
-    def shape(self):
-        return (*self.codes.shape[:-1], self.k)
+    A copy made by empty() or mxfp4_quantize holds both in one buffer, codes first; codes and
+    scales are views of it, made when they are asked for (a call of these operators can be
+    shorter than an allocation and two views)."""
+    __slots__ = ("_codes", "_scales", "k", "n_groups", "_data", "_lead", "_rows")
 
-    def c(self):
-        return MXTensorC(self.codes.data_ptr(), self.scales.data_ptr())
+    def __init__(self, codes, scales, k, n_groups=0):
+        self._codes, self._scales, self.k, self.n_groups, self._data = codes, scales, k, n_groups, None
 
     @staticmethod
     def empty(n, k, device, n_groups=0):
         """Uninitialised copy; n: the number of rows, or a tuple (batch, rows)."""
-        kp = grouped_k(k, n_groups) if n_groups else padded_k(k)
-        n = n if isinstance(n, tuple) else (n,)
-        return MXTensor(_empty(*n, kp // 2, torch.uint8, device), _empty(*n, kp // 32, torch.uint8, device),
-                        k, n_groups)
+        kp = grouped_k(k, n_groups) if n_groups else (k + 127) // 128 * 128
+        t = MXTensor(None, None, k, n_groups)
+        t._lead = n if isinstance(n, tuple) else (n,)
+        t._rows = n if t._lead is not n else math.prod(n)
+        t._data = torch.empty_strided((t._rows * (kp // 32 * 17),), (1,), dtype=torch.uint8, device=device)
+        return t
+
+    def _views(self):
+        kp = grouped_k(self.k, self.n_groups) if self.n_groups else padded_k(self.k)
+        split = self._rows * (kp // 2)
+        self._codes = self._data[:split].view(*self._lead, kp // 2)
+        self._scales = self._data[split:].view(*self._lead, kp // 32)
+
+    @property
+    def codes(self):
+        if self._codes is None:
+            self._views()
+        return self._codes
+
+    @property
+    def scales(self):
+        if self._scales is None:
+            self._views()
+        return self._scales
+
+    @codes.setter
+    def codes(self, value):
+        self._scales, self._codes, self._data = self.scales, value, None
+
+    @scales.setter
+    def scales(self, value):
+        self._codes, self._scales, self._data = self.codes, value, None
+
+    @property
+    def shape(self):
+        return (*(self.codes.shape[:-1] if self._data is None else self._lead), self.k)
+
+    def __repr__(self):
+        return f"MXTensor(shape={self.shape}, n_groups={self.n_groups}, device={_held(self).device})"
+
+
+def _held(t):
+    """A tensor of the copy's memory."""
+    return t.codes if t._data is None else t._data
 
 
 def _empty(*args):
@@ -150,20 +186,31 @@ def _device(t):
 
 def _operand(t, name, device):
     """Checks a copy's tensors (a kernel reads them by their extents alone); returns them as the
-    C struct and the codes' shape."""
-    codes, scales, k = t.codes, t.scales, t.k
+    C struct and the extents before the last."""
+    data, k = t._data, t.k
+    kp = (k + 127) // 128 * 128 if not t.n_groups else grouped_k(k, t.n_groups)
+    if data is not None:
+        if data.get_device() != device:
+            _device(data)
+            raise _error(f"{name} is on another device")
+        split = t._rows * (kp // 2)
+        if data.numel() != split + split // 16:
+            raise _error(f"{name}: its buffer does not hold rows of k = {k}")
+        at = data.data_ptr()
+        return MXTensorC(at, at + split), t._lead
+    codes, scales = t.codes, t.scales
     if codes.get_device() != device or scales.get_device() != device:
         _device(codes), _device(scales)
         raise _error(f"{name} is on another device")
     shape = codes.shape
-    kp = (k + 127) // 128 * 128 if not t.n_groups else grouped_k(k, t.n_groups)
-    if len(shape) < 2 or shape[-1] * 2 != kp or scales.shape != (*shape[:-1], kp // 32):
+    lead = tuple(shape[:-1])
+    if not lead or shape[-1] * 2 != kp or scales.shape != (*lead, kp // 32):
         raise _error(f"{name}: codes {tuple(shape)} and scales {tuple(scales.shape)} do not "
                      f"hold rows of k = {k}")
     if codes.dtype != torch.uint8 or scales.dtype != torch.uint8 or not codes.is_contiguous() \
             or not scales.is_contiguous():
         raise _error(f"{name}: codes and scales must be contiguous uint8 tensors")
-    return MXTensorC(codes.data_ptr(), scales.data_ptr()), shape
+    return MXTensorC(codes.data_ptr(), scales.data_ptr()), lead
 
 
 def _groups(offsets, device):
@@ -237,21 +284,21 @@ def mxfp4_quantize(x, params, offsets=None, row_out=None, col_out=None):
     row = col = rc = cc = None
     if params.rowwise:
         if row_out is None:
-            row = MXTensor.empty((*lead, R), C, x.device)
-            rc = row.c()
+            row = MXTensor.empty((*lead, R) if lead else R, C, x.device)
+            rc = _operand(row, "row_out", dev)[0]
         else:
             row = row_out
             rc, got = _operand(row, "row_out", dev)
-            if got[:-1] != (*lead, R) or row.k != C or row.n_groups:
+            if got != (*lead, R) or row.k != C or row.n_groups:
                 raise _error(f"row_out {row.shape} does not hold x {tuple(shape)}")
     if params.colwise:
         if col_out is None:
-            col = MXTensor.empty((*lead, C), R, x.device, groups)
-            cc = col.c()
+            col = MXTensor.empty((*lead, C) if lead else C, R, x.device, groups)
+            cc = _operand(col, "col_out", dev)[0]
         else:
             col = col_out
             cc, got = _operand(col, "col_out", dev)
-            if got[:-1] != (*lead, C) or col.k != R or col.n_groups != groups:
+            if got != (*lead, C) or col.k != R or col.n_groups != groups:
                 raise _error(f"col_out {col.shape} does not hold x {tuple(shape)} transposed")
     _call(_lib().mxfp4_quantize, dev, x.data_ptr(), dtype, batch, R, C, pitch,
           x.stride(0) if batch > 1 else 0, op, groups, params, rc, cc)
@@ -260,17 +307,18 @@ def mxfp4_quantize(x, params, offsets=None, row_out=None, col_out=None):
 
 def mxfp4_dequantize(q, out_dtype=torch.float32, offsets=None, out=None):
     """The values of a copy, [.., n][k]; a grouped columnwise copy takes its offsets."""
-    dev = _device(q.codes)
-    qc, shape = _operand(q, "q", dev)
+    held = _held(q)
+    dev = _device(held)
+    qc, lead = _operand(q, "q", dev)
     op, groups = _groups(offsets, dev)
     if groups != q.n_groups:
         raise _error(f"the copy has {q.n_groups} groups, offsets {groups}")
-    out, dtype, pitch = _output(out, (*shape[:-1], q.k), out_dtype, q.codes)
-    n = shape[0]
-    if len(shape) > 2:
+    out, dtype, pitch = _output(out, (*lead, q.k), out_dtype, held)
+    n = lead[0]
+    if len(lead) > 1:
         if not out.is_contiguous():
             raise _error("out of a stack of matrices must be contiguous")
-        for d in shape[1:-1]:
+        for d in lead[1:]:
             n *= d
     _call(_lib().mxfp4_dequantize, dev, qc, n, q.k, op, groups, dtype, out.data_ptr(), pitch)
     return out
@@ -278,15 +326,16 @@ def mxfp4_dequantize(q, out_dtype=torch.float32, offsets=None, out=None):
 
 def mxfp4_gemm(a, b, out=None, out_dtype=torch.float32):
     """C = A B^T (A: M x K copy, B: N x K copy)."""
-    dev = _device(a.codes)
+    held = _held(a)
+    dev = _device(held)
     ac, sa = _operand(a, "a", dev)
     bc, sb = _operand(b, "b", dev)
-    if len(sa) != 2 or len(sb) != 2 or a.n_groups or b.n_groups:
+    if len(sa) != 1 or len(sb) != 1 or a.n_groups or b.n_groups:
         raise _error("mxfp4_gemm takes two plain copies")
     if a.k != b.k:
         raise _error(f"K mismatch {a.k} vs {b.k}")
     M, N = sa[0], sb[0]
-    out, dtype, pitch = _output(out, (M, N), out_dtype, a.codes)
+    out, dtype, pitch = _output(out, (M, N), out_dtype, held)
     _call(_lib().mxfp4_gemm, dev, ac, bc, M, N, a.k, out.data_ptr(), dtype, pitch)
     return out
 
@@ -294,18 +343,19 @@ def mxfp4_gemm(a, b, out=None, out_dtype=torch.float32):
 def mxfp4_gemm_grouped(a, b, offsets, out=None, out_dtype=torch.float32):
     """C's rows of group g = A's rows of group g times B[g]^T (A: M x K copy, B: [n_groups] of
     N x K copies).  Rows in no group give 0."""
-    dev = _device(a.codes)
+    held = _held(a)
+    dev = _device(held)
     ac, sa = _operand(a, "a", dev)
     bc, sb = _operand(b, "b", dev)
     op, groups = _groups(offsets, dev)
-    if len(sa) != 2 or len(sb) != 3 or a.n_groups or b.n_groups:
+    if len(sa) != 1 or len(sb) != 2 or a.n_groups or b.n_groups:
         raise _error("mxfp4_gemm_grouped takes a copy of a matrix and one of a stack of matrices")
     if sb[0] != groups:
         raise _error(f"{sb[0]} matrices for {groups} groups")
     if a.k != b.k:
         raise _error(f"K mismatch {a.k} vs {b.k}")
     M, N = sa[0], sb[1]
-    out, dtype, pitch = _output(out, (M, N), out_dtype, a.codes)
+    out, dtype, pitch = _output(out, (M, N), out_dtype, held)
     _call(_lib().mxfp4_gemm_grouped, dev, ac, bc, op, groups, M, N, a.k, out.data_ptr(), dtype, pitch)
     return out
 
@@ -313,16 +363,17 @@ def mxfp4_gemm_grouped(a, b, offsets, out=None, out_dtype=torch.float32):
 def mxfp4_gemm_grouped_wgrad(a, b, offsets, out=None, out_dtype=torch.float32):
     """C[g] = A_g B_g^T over group g's span of two grouped columnwise copies (A: [M][rows],
     B: [N][rows]); returns [n_groups][M][N], 0 for an empty group."""
-    dev = _device(a.codes)
+    held = _held(a)
+    dev = _device(held)
     ac, sa = _operand(a, "a", dev)
     bc, sb = _operand(b, "b", dev)
     op, groups = _groups(offsets, dev)
-    if len(sa) != 2 or len(sb) != 2 or a.n_groups != groups or b.n_groups != groups or not groups:
+    if len(sa) != 1 or len(sb) != 1 or a.n_groups != groups or b.n_groups != groups or not groups:
         raise _error("mxfp4_gemm_grouped_wgrad takes two columnwise copies made with these offsets")
     if a.k != b.k:
         raise _error(f"row mismatch {a.k} vs {b.k}")
     M, N = sa[0], sb[0]
-    out, dtype, _ = _output(out, (groups, M, N), out_dtype, a.codes)
+    out, dtype, _ = _output(out, (groups, M, N), out_dtype, held)
     if not out.is_contiguous():
         raise _error("out must be contiguous")
     _call(_lib().mxfp4_gemm_grouped_wgrad, dev, ac, bc, op, groups, M, N, a.k, out.data_ptr(), dtype, N)
@@ -342,10 +393,10 @@ def mxfp4_linear(x, w, offsets=None, scale_rule=MXFP4_SCALE_FLOOR, out=None, out
         raise _error("x must be a 2-D tensor")
     wc, sw = _operand(w, "w", dev)
     op, groups = _groups(offsets, dev)
-    if len(sw) != (3 if groups else 2) or w.n_groups or (groups and sw[0] != groups):
+    if len(sw) != (2 if groups else 1) or w.n_groups or (groups and sw[0] != groups):
         raise _error("w must be one copy, or with offsets a stack of one copy per group")
     M, K = shape
-    N = sw[-2]
+    N = sw[-1]
     if w.k != K:
         raise _error(f"K mismatch {K} vs {w.k}")
     out, dtype, pitch = _output(out, (M, N), out_dtype or x.dtype, x)

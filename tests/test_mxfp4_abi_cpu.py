@@ -159,3 +159,21 @@ def test_calls_run_on_their_tensors_device(monkeypatch):
     mxfp4._call(f, 0, 5)
     mxfp4._call(f, 1, 6)
     assert seen == [([], (5, 100)), ([1], (6, 101))] and entered == [1, "left"]
+
+
+def test_copies_hold_codes_and_scales_in_one_buffer():
+    import torch
+    import nvfp4_block_scaled_quantize_amd as nv
+    for n, k, groups in ((5, 300, 0), ((2, 3), 64, 0), (7, 130, 4), (0, 10, 0), (4, 0, 0), ((0, 3), 5, 0)):
+        kp = (k + min(k, groups) * 127) // 128 * 128 if groups else (k + 127) // 128 * 128
+        lead = n if isinstance(n, tuple) else (n,)
+        t = nv.MXTensor.empty(n, k, "cpu", groups)
+        assert t.shape == (*lead, k) and t.codes.shape == (*lead, kp // 2) and t.scales.shape == (*lead, kp // 32)
+        t.codes.fill_(1), t.scales.fill_(2)
+        assert t.codes.is_contiguous() and t.scales.is_contiguous()
+        assert (t.codes == 1).all() and (t.scales == 2).all()          # they do not overlap
+        assert t.codes.numel() == 0 or t.scales.data_ptr() == t.codes.data_ptr() + t.codes.numel()
+        c = torch.zeros_like(t.codes)
+        t.codes = c                                                      # assigned ones are taken as they are
+        assert t.codes is c and (t.scales == 2).all() and t.shape == (*lead, k)
+    assert "MXTensor" in repr(nv.MXTensor.empty(3, 5, "cpu"))
