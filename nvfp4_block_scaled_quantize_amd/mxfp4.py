@@ -159,13 +159,6 @@ def _held(t):
     return t.codes if t._data is None else t._data
 
 
-def _empty(*args):
-    """torch.empty(shape, dtype, device) for two or three extents (0.4 us sooner)."""
-    *shape, dtype, device = args
-    strides = (shape[1], 1) if len(shape) == 2 else (shape[1] * shape[2], shape[2], 1)
-    return torch.empty_strided(shape, strides, dtype=dtype, device=device)
-
-
 def padded_k(k):
     """mxfp4_padded_k: the K extent of a copy's rows."""
     return (k + 127) // 128 * 128
@@ -202,15 +195,14 @@ def _operand(t, name, device):
     if codes.get_device() != device or scales.get_device() != device:
         _device(codes), _device(scales)
         raise _error(f"{name} is on another device")
-    shape = codes.shape
-    lead = tuple(shape[:-1])
-    if not lead or shape[-1] * 2 != kp or scales.shape != (*lead, kp // 32):
-        raise _error(f"{name}: codes {tuple(shape)} and scales {tuple(scales.shape)} do not "
+    *lead, width = codes.shape
+    if not lead or width * 2 != kp or scales.shape != (*lead, kp // 32):
+        raise _error(f"{name}: codes {tuple(codes.shape)} and scales {tuple(scales.shape)} do not "
                      f"hold rows of k = {k}")
     if codes.dtype != torch.uint8 or scales.dtype != torch.uint8 or not codes.is_contiguous() \
             or not scales.is_contiguous():
         raise _error(f"{name}: codes and scales must be contiguous uint8 tensors")
-    return MXTensorC(codes.data_ptr(), scales.data_ptr()), lead
+    return MXTensorC(codes.data_ptr(), scales.data_ptr()), tuple(lead)
 
 
 def _groups(offsets, device):
@@ -231,13 +223,14 @@ def _matrix(x, name):
     if dtype is None:
         raise _error(f"unsupported dtype {x.dtype}")
     device, shape = _device(x), x.shape
-    if len(shape) < 2:
+    if len(shape) == 2:
+        (rows, cols), (pitch, step) = shape, x.stride()
+    elif len(shape) < 2:
         raise _error(f"{name} must be a matrix")
-    rows, cols = shape[-2:]
-    strides = x.stride()
-    if cols > 1 and strides[-1] != 1:
+    else:
+        (rows, cols), (pitch, step) = shape[-2:], x.stride()[-2:]
+    if cols > 1 and step != 1:
         raise _error(f"{name} must have unit column stride")
-    pitch = strides[-2]
     if pitch < cols:
         if rows > 1:
             raise _error(f"{name}'s rows overlap (row stride below the number of columns)")
@@ -251,9 +244,11 @@ def _output(out, shape, dtype, like):
         code = _DTYPES.get(dtype)
         if code is None:
             raise _error(f"unsupported dtype {dtype}")
-        if len(shape) > 3:
-            return torch.empty(shape, dtype=dtype, device=like.device), code, shape[-1]
-        return _empty(*shape, dtype, like.device), code, shape[-1]
+        if len(shape) == 2:     # empty_strided takes 0.4 us less than empty
+            out = torch.empty_strided(shape, (shape[1], 1), dtype=dtype, device=like.device)
+        else:
+            out = torch.empty(shape, dtype=dtype, device=like.device)
+        return out, code, shape[-1]
     device, got, code, pitch = _matrix(out, "out")
     if got != shape or device != like.get_device():
         raise _error(f"out must be a {shape} tensor on the operands' device")
@@ -403,7 +398,7 @@ def mxfp4_linear(x, w, offsets=None, scale_rule=MXFP4_SCALE_FLOOR, out=None, out
     lib = _lib()
     if workspace is None:
         need = lib.mxfp4_linear_workspace_bytes(M, N, K, groups)
-        workspace = _empty(1, need, torch.uint8, x.device) if need else None
+        workspace = torch.empty_strided((need,), (1,), dtype=torch.uint8, device=x.device) if need else None
     elif workspace.get_device() != dev or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise _error("workspace must be a contiguous uint8 tensor on x's device")
     ws, ws_bytes = (workspace.data_ptr(), workspace.numel()) if workspace is not None else (None, 0)
