@@ -70,7 +70,7 @@ extern "C" int mxfp4_gemm(const mxfp4_tensor* a, const mxfp4_tensor* b, int64_t 
     // workgroup: 16 x 6144 x 4096 6.1 us against 10.7, 77 x 4999 x 2056 (471 of its workgroups) 6.0
     // against 8.9, 256 x 1024 x 4096 (256) 5.8 against 10.7; but 64 x 9216 x 2048 (576) 7.8 either way,
     // 128 x 6144 x 4096 (768) 12.8 against 11.5.
-    if (mx_few_dense(M, N, g.kp)) return mx_few_packed({g, nullptr, 0, K, 0}, c_dtype, (hipStream_t)stream);
+    if (K > 0 && mx_few_dense(M, N, g.kp)) return mx_few_packed({g, nullptr, 0, K, 0}, c_dtype, (hipStream_t)stream);
     return launch_gemm<MxDense>(g, c_dtype, (hipStream_t)stream);
 }
 
@@ -89,7 +89,7 @@ extern "C" int mxfp4_gemm_grouped(const mxfp4_tensor* a, const mxfp4_tensor* b, 
     // groups: 80 rows 14.2 us against 19.8, 400 rows 17.8 against 20.2; 2048 x 6144, 8 groups: 16 rows
     // 11.4 against 15.0; 9216 x 4096, 4 groups: 32 rows 17.3 against 19.3, 64 rows (64 Ki a group)
     // 21.2 against 19.5).
-    if (M * g.kp <= busy * (g.kp > 48 << 10 ? g.kp : 48 << 10) && mx_few_fits(M, g.kp))
+    if (K > 0 && M * g.kp <= busy * (g.kp > 48 << 10 ? g.kp : 48 << 10) && mx_few_fits(M, g.kp))
         return mx_few_packed({g, nullptr, 0, K, 0}, c_dtype, (hipStream_t)stream);
     return launch_gemm<MxRows>(g, c_dtype, (hipStream_t)stream);
 }

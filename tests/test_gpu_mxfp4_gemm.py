@@ -425,6 +425,17 @@ def test_empty(nv):
     assert (c == 0).all()
 
 
+def test_no_k(nv):
+    """Products over K = 0 are zeros at every size."""
+    d = dev()
+    e = lambda n: nv.MXTensor.empty(n, 0, d)
+    off = torch.tensor([0, 2, 5], dtype=torch.int32, device=d)
+    for M, N in ((1, 1), (16, 300), (40, 700), (600, 700), (4096, 4100)):
+        for dt, _ in DTYPES:
+            assert (nv.mxfp4_gemm(e(M), e(N), out=torch.ones(M, N, device=d, dtype=dt)) == 0).all()
+            assert (nv.mxfp4_gemm_grouped(e(M), e((2, N)), off, out=torch.ones(M, N, device=d, dtype=dt)) == 0).all()
+
+
 def test_refusals(nv):
     d = dev()
     e = lambda n, k, g=0: nv.MXTensor.empty(n, k, d, g)
