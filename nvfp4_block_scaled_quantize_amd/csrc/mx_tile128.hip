@@ -241,8 +241,10 @@ static int launch(const MxGArgs& g, hipStream_t st) {
     if (!mx_grid_fits(tiles, 256)) return NVFP4_ERR_SHAPE;
     const int units = mx_compute_units();
     if (!units) return NVFP4_ERR_HIP;
-    return tiles <= units ? launch_slots<T, MODE, STREAM, 4>(g, tiles, st)
-                          : launch_slots<T, MODE, STREAM, 2>(g, tiles, st);
+    // (float32 streams from 128 MB on, which is thousands of tiles)
+    if constexpr (sizeof(T) == 2 || !STREAM)
+        if (tiles <= units) return launch_slots<T, MODE, STREAM, 4>(g, tiles, st);
+    return launch_slots<T, MODE, STREAM, 2>(g, tiles, st);
 }
 
 template <typename T, bool STREAM>
