@@ -113,12 +113,7 @@ class MXTensor:
     @staticmethod
     def empty(n, k, device, n_groups=0):
         """Uninitialised copy; n: the number of rows, or a tuple (batch, rows)."""
-        kp = grouped_k(k, n_groups) if n_groups else (k + 127) // 128 * 128
-        t = MXTensor(None, None, k, n_groups)
-        t._lead = n if isinstance(n, tuple) else (n,)
-        t._rows = n if t._lead is not n else math.prod(n)
-        t._data = torch.empty_strided((t._rows * (kp // 32 * 17),), (1,), dtype=torch.uint8, device=device)
-        return t
+        return _new(n if isinstance(n, tuple) else (n,), k, device, n_groups)[0]
 
     def _views(self):
         kp = grouped_k(self.k, self.n_groups) if self.n_groups else padded_k(self.k)
@@ -152,6 +147,18 @@ class MXTensor:
 
     def __repr__(self):
         return f"MXTensor(shape={self.shape}, n_groups={self.n_groups}, device={_held(self).device})"
+
+
+def _new(lead, k, device, n_groups):
+    """An uninitialised copy and its C struct."""
+    kp = grouped_k(k, n_groups) if n_groups else (k + 127) // 128 * 128
+    rows = lead[0] if len(lead) == 1 else math.prod(lead)
+    split = rows * (kp // 2)
+    t = MXTensor(None, None, k, n_groups)
+    t._lead, t._rows = lead, rows
+    t._data = torch.empty_strided((split + split // 16,), (1,), dtype=torch.uint8, device=device)
+    at = t._data.data_ptr()
+    return t, MXTensorC(at, at + split)
 
 
 def _held(t):
@@ -279,8 +286,7 @@ def mxfp4_quantize(x, params, offsets=None, row_out=None, col_out=None):
     row = col = rc = cc = None
     if params.rowwise:
         if row_out is None:
-            row = MXTensor.empty((*lead, R) if lead else R, C, x.device)
-            rc = _operand(row, "row_out", dev)[0]
+            row, rc = _new((*lead, R), C, x.device, 0)
         else:
             row = row_out
             rc, got = _operand(row, "row_out", dev)
@@ -288,8 +294,7 @@ def mxfp4_quantize(x, params, offsets=None, row_out=None, col_out=None):
                 raise _error(f"row_out {row.shape} does not hold x {tuple(shape)}")
     if params.colwise:
         if col_out is None:
-            col = MXTensor.empty((*lead, C) if lead else C, R, x.device, groups)
-            cc = _operand(col, "col_out", dev)[0]
+            col, cc = _new((*lead, C), R, x.device, groups)
         else:
             col = col_out
             cc, got = _operand(col, "col_out", dev)
