@@ -318,8 +318,8 @@ def mxfp4_dequantize(q, out_dtype=torch.float32, offsets=None, out=None):
     if len(lead) > 1:
         if not out.is_contiguous():
             raise _error("out of a stack of matrices must be contiguous")
-        for d in lead[1:]:
-            n *= d
+        # all its rows are one run; the stride of an axis of length 1 says nothing of them
+        n, pitch = math.prod(lead), q.k
     _call(_lib().mxfp4_dequantize, dev, qc, n, q.k, op, groups, dtype, out.data_ptr(), pitch)
     return out
 
