@@ -143,9 +143,10 @@ def load_library(path: Optional[str] = None):
     if lib.nvfp4_abi_version() != ABI_VERSION:
         raise Nvfp4Error(f"{p} has ABI version {lib.nvfp4_abi_version()}, this binding expects "
                          f"{ABI_VERSION}: rebuild the HIP library (__graft_entry__.build())")
-    _mxfp4.bind(lib)
+    unusable = _mxfp4.bind(lib)
     if path is None:
-        _lib = _mxfp4._bound = lib
+        _lib = lib
+        _mxfp4.attach(lib, unusable)
     return lib
 
 

@@ -46,7 +46,14 @@ def _error(msg):
 
 
 def bind(lib):
-    """Declares the MXFP4 functions' types on a loaded libnvfp4.so."""
+    """Declares the MXFP4 functions' types on a loaded libnvfp4.so.  Returns what keeps this
+    binding from using them, or None: the NVFP4 calls need none of them."""
+    lacking = [name for name in MXFP4_EXPORTED if not hasattr(lib, name)]
+    if lacking:
+        return f"the library lacks {lacking[0]}: rebuild it (__graft_entry__.build())"
+    if lib.mxfp4_abi_version() != MXFP4_ABI_VERSION:
+        return (f"the library has MXFP4 ABI version {lib.mxfp4_abi_version()}, this binding expects "
+                f"{MXFP4_ABI_VERSION}: rebuild it (__graft_entry__.build())")
     vp, i64, i32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
     it = ctypes.c_int
     T, Q = ctypes.POINTER(MXTensorC), ctypes.POINTER(MxQuantParams)
@@ -61,22 +68,27 @@ def bind(lib):
             ("mxfp4_linear_workspace_bytes", sz, [i64, i64, i64, i64]),
             ("mxfp4_linear", it, [vp, it, i64, i64, i64, i32, T, i64, vp, i64, vp, it, i64, vp, sz, vp]),
             ("mxfp4_abi_version", it, [])]:
-        if not hasattr(lib, name):
-            raise _error(f"the library lacks {name}: rebuild it (__graft_entry__.build())")
         f = getattr(lib, name)
         f.restype, f.argtypes = res, args
-    if lib.mxfp4_abi_version() != MXFP4_ABI_VERSION:
-        raise _error(f"the library has MXFP4 ABI version {lib.mxfp4_abi_version()}, this binding "
-                     f"expects {MXFP4_ABI_VERSION}: rebuild it (__graft_entry__.build())")
+    return None
 
 
-_bound = None   # the package's library once it is loaded
+_bound = None      # the package's library once it is loaded and these calls can use it
+_unusable = None   # or why they cannot
+
+
+def attach(lib, unusable):
+    """Takes the package's library, with what bind() said of it."""
+    global _bound, _unusable
+    _bound, _unusable = (None if unusable else lib), unusable
 
 
 def _lib():
     if _bound is None:
         from . import load_library
         load_library()
+        if _bound is None:
+            raise _error(_unusable)
     return _bound
 
 
