@@ -20,7 +20,10 @@
  * Elements past k are zero codes; blocks wholly past k have scale code 0.  The rowwise copy
  * of an R x C matrix X is X quantized along its rows (n = R, k = C); the columnwise copy is
  * X^T quantized along its rows (n = C, k = R).  Extents may be any size, row pitches any
- * pitch, and inputs need only their element's alignment.
+ * pitch of at least a row, and inputs need only their element's alignment.  Only sizes far
+ * past a device's memory, or made almost wholly of padding, are refused (NVFP4_ERR_SHAPE): an
+ * extent above 2^34 - 2^13, a C of more than 2^40 elements, a launch of 2^32 threads or more
+ * (such as 2^30 rows of one column).
  *
  * Groups.  `offsets` is a device array of n_groups + 1 int32: group g holds the rows
  * [offsets[g], offsets[g+1]) of a matrix (an expert's tokens).  offsets[0] is read as 0;
@@ -128,7 +131,8 @@ int mxfp4_gemm_grouped_wgrad(const mxfp4_tensor* a, const mxfp4_tensor* b, const
  * grouped as in mxfp4_gemm_grouped with W holding n_groups matrices.  The result is that of
  * mxfp4_quantize followed by the product.
  *   ws  device workspace of mxfp4_linear_workspace_bytes() bytes, 256-byte aligned (0 bytes,
- *       NULL allowed, for the few rows that are quantized inside the product's kernel) */
+ *       NULL allowed, for the few rows that are quantized inside the product's kernel, and for
+ *       sizes that the call refuses) */
 size_t mxfp4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t n_groups);
 int mxfp4_linear(const void* x, int dtype, int64_t M, int64_t K, int64_t ld_x, int32_t scale_rule,
                  const mxfp4_tensor* w, int64_t N, const int32_t* offsets, int64_t n_groups,

@@ -14,6 +14,11 @@ constexpr int64_t kMxMaxK = (int64_t)1 << 23;   // 256 rows of codes stay within
 
 typedef int int8v __attribute__((ext_vector_type(8)));
 
+// No extent is larger: a quarter of a padded row (the decode's pieces) and what a workgroup adds to it
+// are counted in 32 bits.
+constexpr int64_t kMxMaxExtent = ((int64_t)1 << 34) - (1 << 13);
+constexpr int64_t kMxMaxC = (int64_t)1 << 40;   // elements of a product's C, so that counts of them stay in 64 bits
+
 inline int64_t mx_pad(int64_t k) { return (k + kMxPad - 1) / kMxPad * kMxPad; }
 
 // E8M0 code of a block from the binary32 bits of its largest magnitude (magnitudes order as
@@ -354,8 +359,8 @@ inline int mx_compute_units() {
     return n;
 }
 
-// A grid's threads are counted in 32 bits.
-inline bool mx_grid_fits(int64_t blocks, int threads) { return blocks * threads < ((int64_t)1 << 32); }
+// A grid's threads are counted in 32 bits.  (Wide: products of extents.)
+inline bool mx_grid_fits(__int128 blocks, int threads) { return blocks * threads < ((__int128)1 << 32); }
 
 typedef float float4v __attribute__((ext_vector_type(4)));
 
@@ -393,6 +398,7 @@ __device__ __forceinline__ void store_c16(T* p, int4v v, int64_t left) {
 }
 
 // ---------------------------------------------------------------- host checks
+inline bool mx_extent(int64_t n) { return n >= 0 && n <= kMxMaxExtent; }
 // `used`: the copy has elements, so its arrays must exist.
 inline int mx_check_tensor(const mxfp4_tensor* t, bool used) {
     if (!t || (used && (!t->codes || !t->scales))) return NVFP4_ERR_NULL;

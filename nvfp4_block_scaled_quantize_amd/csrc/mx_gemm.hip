@@ -42,10 +42,15 @@ static int launch_gemm(const MxGArgs& g, int c_dtype, hipStream_t st) {
     return mx_tile128(g, MODE, c_dtype, streams(g, MODE), st);
 }
 
+// Whether a product's extents are ones that the launch code can count with.
+static bool gemm_extents(int64_t M, int64_t N, int64_t K) {
+    return mx_extent(M) && mx_extent(N) && K >= 0 && K <= kMxMaxK && (N == 0 || M <= kMxMaxC / N);
+}
+
 // Checks shared by the products; *empty when C has no elements.
 static int check_gemm(const mxfp4_tensor* a, const mxfp4_tensor* b, int64_t M, int64_t N, int64_t K,
                       const void* c, int c_dtype, int64_t ldc, bool* empty) {
-    if (M < 0 || N < 0 || K < 0 || ldc < N || K > kMxMaxK) return NVFP4_ERR_SHAPE;
+    if (!gemm_extents(M, N, K) || ldc < N) return NVFP4_ERR_SHAPE;
     const int size = mx_dtype_size(c_dtype);
     if (!size) return NVFP4_ERR_DTYPE;
     if (int rc = mx_check_tensor(a, M && K)) return rc;
@@ -98,7 +103,7 @@ extern "C" int mxfp4_gemm_grouped_wgrad(const mxfp4_tensor* a, const mxfp4_tenso
                                         const int32_t* offsets, int64_t n_groups, int64_t M, int64_t N,
                                         int64_t rows, void* c, int c_dtype, int64_t ldc, void* stream) {
     bool empty;
-    if (rows < 0 || n_groups < 1) return NVFP4_ERR_SHAPE;
+    if (!mx_extent(rows) || n_groups < 1) return NVFP4_ERR_SHAPE;
     if (int rc = mx_check_groups(offsets, n_groups, rows)) return rc;
     const int64_t kp = mxfp4_grouped_k(rows, n_groups);
     if (int rc = check_gemm(a, b, M, N, kp, c, c_dtype, ldc, &empty)) return rc;
@@ -131,6 +136,7 @@ static bool linear_fused(int64_t M, int64_t N, int64_t K, int64_t n_groups) {
 }
 
 extern "C" size_t mxfp4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t n_groups) {
+    if (!gemm_extents(M, N, K)) return 0;       // mxfp4_linear refuses them
     return M > 0 && K > 0 && !linear_fused(M, N, K, n_groups) ? linear_code_bytes(M, K) + (size_t)(M * (mx_pad(K) / 32)) : 0;
 }
 
@@ -138,7 +144,7 @@ extern "C" int mxfp4_linear(const void* x, int dtype, int64_t M, int64_t K, int6
                             int32_t scale_rule, const mxfp4_tensor* w, int64_t N, const int32_t* offsets,
                             int64_t n_groups, void* c, int c_dtype, int64_t ldc, void* ws,
                             size_t ws_bytes, void* stream) {
-    if (M < 0 || K < 0) return NVFP4_ERR_SHAPE;
+    if (!gemm_extents(M, N, K)) return NVFP4_ERR_SHAPE;
     const size_t need = mxfp4_linear_workspace_bytes(M, N, K, n_groups);
     if (need && (!ws || ws_bytes < need)) return NVFP4_ERR_WORKSPACE;
     if ((uintptr_t)ws & 255) return NVFP4_ERR_ALIGN;

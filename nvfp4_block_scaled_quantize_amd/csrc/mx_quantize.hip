@@ -348,30 +348,39 @@ __global__ __launch_bounds__(256) void k_mx_decode_grouped(MxDArgs g, unsigned u
 }
 
 template <typename T>
-static void launch_decode(const MxDArgs& g, hipStream_t st) {
+static int launch_decode(const MxDArgs& g, hipStream_t st) {
     if (g.n_groups) {
         // one unit more than the copy holds: the rows in no group
-        const unsigned row_tiles = (unsigned)((g.n + kDecodeSteps - 1) / kDecodeSteps);
-        const unsigned unit_tiles = (unsigned)((g.kp / kMxPad + 4 * kDecodeUnits<T>) / (4 * kDecodeUnits<T>));
-        k_mx_decode_grouped<T><<<dim3(unit_tiles * row_tiles), 256, 0, st>>>(g, unit_tiles, row_tiles);
+        const int64_t row_tiles = (g.n + kDecodeSteps - 1) / kDecodeSteps;
+        const int64_t unit_tiles = (g.kp / kMxPad + 4 * kDecodeUnits<T>) / (4 * kDecodeUnits<T>);
+        const __int128 grid = (__int128)unit_tiles * row_tiles;
+        if (!mx_grid_fits(grid, 256)) return NVFP4_ERR_SHAPE;
+        k_mx_decode_grouped<T><<<dim3((unsigned)grid), 256, 0, st>>>(g, (unsigned)unit_tiles, (unsigned)row_tiles);
     } else {
-        const int64_t pieces = g.n * (g.kp / Piece<T>::n), per = 256 * kRowSteps;
-        k_mx_decode<T><<<dim3((unsigned)((pieces + per - 1) / per)), 256, 0, st>>>(g);
+        const int per = 256 * kRowSteps;
+        const __int128 grid = ((__int128)g.n * (g.kp / Piece<T>::n) + per - 1) / per;
+        if (!mx_grid_fits(grid, 256)) return NVFP4_ERR_SHAPE;
+        k_mx_decode<T><<<dim3((unsigned)grid), 256, 0, st>>>(g);
     }
+    return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
 }
 
 template <typename T, bool SR>
-static void launch_quantize(const MxQArgs& g, hipStream_t st) {
+static int launch_quantize(const MxQArgs& g, hipStream_t st) {
     if (!g.cc) {
-        const int64_t octs = g.batch * g.rows * (g.row_kp / 8), per = 256 * kRowSteps;
-        k_mx_rows<T, SR><<<dim3((unsigned)((octs + per - 1) / per)), 256, 0, st>>>(g);
-        return;
+        const int per = 256 * kRowSteps;
+        const __int128 grid = ((__int128)g.batch * g.rows * (g.row_kp / 8) + per - 1) / per;
+        if (!mx_grid_fits(grid, 256)) return NVFP4_ERR_SHAPE;
+        k_mx_rows<T, SR><<<dim3((unsigned)grid), 256, 0, st>>>(g);
+    } else {
+        // units cover the rows in no group too (one more partial unit at most); tiles cover the
+        // rowwise copy's padding
+        const int64_t units = g.col_kp / kMxPad, col_tiles = g.row_kp * (int64_t)sizeof(T) / 256;
+        const __int128 grid = (g.n_groups ? units + 1 : (__int128)units * g.batch) * col_tiles;
+        if (!mx_grid_fits(grid, 256)) return NVFP4_ERR_SHAPE;
+        k_mx_tile<T, SR><<<dim3((unsigned)grid), 256, 0, st>>>(g, (unsigned)units, (unsigned)col_tiles);
     }
-    // units cover the rows in no group too (one more partial unit at most); tiles cover the
-    // rowwise copy's padding
-    const unsigned units = (unsigned)(g.col_kp / kMxPad), col_tiles = (unsigned)(g.row_kp * sizeof(T) / 256);
-    const int64_t grid = (g.n_groups ? units + 1 : units * g.batch) * (int64_t)col_tiles;
-    k_mx_tile<T, SR><<<dim3((unsigned)grid), 256, 0, st>>>(g, units, col_tiles);
+    return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
 }
 
 }  // namespace nvfp4
@@ -393,7 +402,7 @@ extern "C" int mxfp4_quantize(const void* x, int dtype, int64_t batch, int64_t r
                               int64_t n_groups, const mxfp4_quant_params* p,
                               const mxfp4_tensor* row_out, const mxfp4_tensor* col_out, void* stream) {
     if (!p) return NVFP4_ERR_NULL;
-    if (batch < 0 || rows < 0 || cols < 0 || ld_x < cols) return NVFP4_ERR_SHAPE;
+    if (!mx_extent(batch) || !mx_extent(rows) || !mx_extent(cols) || ld_x < cols) return NVFP4_ERR_SHAPE;
     const int size = mx_dtype_size(dtype);
     if (!size) return NVFP4_ERR_DTYPE;
     const auto flag = [](int32_t v) { return v == 0 || v == 1; };
@@ -424,17 +433,16 @@ extern "C" int mxfp4_quantize(const void* x, int dtype, int64_t batch, int64_t r
     // An input of half the last-level cache (256 MB) or more is not still there from its
     // producer, whose own operands went through as well: past the caches 8192 x 9216 bfloat16
     // takes 50 us against 58 when it comes from memory, but 47 against 39 when it is cached.
-    g.stream = batch * rows * cols * size >= ((int64_t)128 << 20);
+    g.stream = (__int128)batch * rows * cols * size >= ((int64_t)128 << 20);
     const bool sr = (g.rc && g.sr_row) || (g.cc && g.sr_col);
-    if (dtype == NVFP4_BF16) sr ? launch_quantize<uint16_t, true>(g, st) : launch_quantize<uint16_t, false>(g, st);
-    else sr ? launch_quantize<float, true>(g, st) : launch_quantize<float, false>(g, st);
-    return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
+    if (dtype == NVFP4_BF16) return sr ? launch_quantize<uint16_t, true>(g, st) : launch_quantize<uint16_t, false>(g, st);
+    return sr ? launch_quantize<float, true>(g, st) : launch_quantize<float, false>(g, st);
 }
 
 extern "C" int mxfp4_dequantize(const mxfp4_tensor* q, int64_t n, int64_t k, const int32_t* offsets,
                                 int64_t n_groups, int out_dtype, void* out, int64_t ld_out,
                                 void* stream) {
-    if (n < 0 || k < 0 || ld_out < k) return NVFP4_ERR_SHAPE;
+    if (!mx_extent(n) || !mx_extent(k) || ld_out < k) return NVFP4_ERR_SHAPE;
     const int size = mx_dtype_size(out_dtype);
     if (!size) return NVFP4_ERR_DTYPE;
     if (int rc = mx_check_groups(offsets, n_groups, k)) return rc;
@@ -445,7 +453,5 @@ extern "C" int mxfp4_dequantize(const mxfp4_tensor* q, int64_t n, int64_t k, con
     MxDArgs g = {q->codes, q->scales, n, k, n_groups ? mxfp4_grouped_k(k, n_groups) : mx_pad(k),
                  offsets, (int)n_groups, out, ld_out};
     const hipStream_t st = (hipStream_t)stream;
-    if (out_dtype == NVFP4_BF16) launch_decode<uint16_t>(g, st);
-    else launch_decode<float>(g, st);
-    return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
+    return out_dtype == NVFP4_BF16 ? launch_decode<uint16_t>(g, st) : launch_decode<float>(g, st);
 }
