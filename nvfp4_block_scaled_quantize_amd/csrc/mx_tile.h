@@ -11,10 +11,12 @@ constexpr int kRow = 128;               // code bytes of a row and stage: 256 el
 // positive this way.
 constexpr uint32_t kBias = 3072;
 
-// dma16 in two: M0, and a load at an offset that moves both its addresses.  Nothing that the
-// compiler makes of these kernels writes M0.
+// dma16 in two: M0, and a load at an offset that moves both its addresses.  Several loads rely on one
+// set_m0, so nothing that the compiler makes of these kernels may write M0 in between; a test looks
+// through their code for it.  (Taking M0's content from set_m0 into each load as an operand would let
+// the compiler see that too, but holds one more scalar register: 0.5 to 1 % of the large products.)
 __device__ __forceinline__ void set_m0(uint32_t lds_addr) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0" ::"s"(lds_addr) : "memory");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0" ::"s"(lds_addr) : "memory", "m0");
 }
 template <int OFFSET>
 __device__ __forceinline__ void dma16_at(int4v rsrc, uint32_t voff, uint32_t soff) {
