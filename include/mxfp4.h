@@ -129,7 +129,7 @@ int mxfp4_gemm_grouped_wgrad(const mxfp4_tensor* a, const mxfp4_tensor* b, const
 /* The forward of a layer in one call: C[M][N] = Q(X) W^T with X (bf16 or f32, M x K, row pitch
  * ld_x) quantized rowwise to nearest even by scale_rule, W a copy N x K; or, with offsets,
  * grouped as in mxfp4_gemm_grouped with W holding n_groups matrices.  The result is that of
- * mxfp4_quantize followed by the product.
+ * mxfp4_quantize followed by the product, bit for bit.
  *   ws  device workspace of mxfp4_linear_workspace_bytes() bytes, 256-byte aligned (0 bytes,
  *       NULL allowed, for the few rows that are quantized inside the product's kernel, and for
  *       sizes that the call refuses) */
