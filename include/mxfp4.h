@@ -94,7 +94,8 @@ int mxfp4_quantize(const void* x, int dtype, int64_t batch, int64_t rows, int64_
                    const mxfp4_tensor* col_out, void* stream);
 
 /* Decode one copy: out[n][k] (f32 or bf16 per out_dtype, row pitch ld_out >= k) gets the
- * values the codes stand for, exact in f32 and, for a copy made of bf16 values, in bf16.  For
+ * values the codes stand for, exact in f32 and, for a copy made of bf16 values, in bf16; but
+ * 2^128 and more, to which CEIL can round magnitudes above 1.5 * 2^127, become infinite.  For
  * a grouped columnwise copy pass its offsets and k = the number of rows; positions of rows in
  * no group get 0. */
 int mxfp4_dequantize(const mxfp4_tensor* q, int64_t n, int64_t k, const int32_t* offsets,

@@ -10,8 +10,8 @@
 // elements of K at 32 (l / 16), with their scale byte.
 //
 // Measured (GPU time per call in a replayed graph, three sets of operands in turn): 1 x 6144 x
-// 4096, x in bfloat16, 5.3 us (W alone at the card's copy rate: 2.8 us, an empty kernel: about 2.4
-// us) against 8.2 as quantize and packed product; 16 rows, packed, 6.1 us against 10.7 by tiles; 24
+// 4096, x in bfloat16, 5.3 us (W alone at the rate of plain reads: 1.9 us, an empty kernel: about
+// 2.4 us) against 8.2 as quantize and packed product; 16 rows, packed, 6.1 us against 10.7 by tiles; 24
 // rows over 17 groups (4096 x 2048, 71 MB of W) 15.0 us.  With branches around the loads, whose
 // joins wait for them, the packed 16 rows took 10.2 us.
 #include "mx_common.h"
@@ -235,12 +235,13 @@ static int launch(const MxFArgs& f, int64_t units, hipStream_t st) {
     return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
 }
 
-// The tile of a dense product.  Up to 16 rows: 16 columns a workgroup.  Eight waves halve a wave's K
-// (1 x 1024 x 8192 4.6 against 5.0 us, 16 x 6144 x 4096 6.1 against 6.3), but with more than about 448
-// workgroups four are enough and start sooner (1 x 16384 x 2048 5.3 against 6.5 us, 4 x 9216 x 2048
-// 4.9 against 5.2).  More rows: the smallest tile that leaves no compute unit two workgroups, or else
-// 32 x 32.  Packed, 32 x 1024 x 4096: 16 x 16 4.0 us, 32 x 16 4.5; 128 x 1024 x 4096: 5.5, 4.7, 32 x 32
-// 5.7; 64 x 6144 x 4096: 13.0, 9.4, 9.1.
+// The tile of a dense product (counts of workgroups: for an MI355X's 256 compute units).  Up to 16
+// rows: 16 columns a workgroup.  Eight waves halve a wave's K (1 x 1024 x 8192 4.6 against 5.0 us,
+// 16 x 6144 x 4096 6.1 against 6.3), but with more than about 448 workgroups four are enough and
+// start sooner (1 x 16384 x 2048 5.3 against 6.5 us, 4 x 9216 x 2048 4.9 against 5.2).  More rows:
+// the smallest tile that leaves no compute unit two workgroups, or else 32 x 32.  Packed, 32 x 1024
+// x 4096: 16 x 16 4.0 us, 32 x 16 4.5; 128 x 1024 x 4096: 5.5, 4.7, 32 x 32 5.7; 64 x 6144 x 4096:
+// 13.0, 9.4, 9.1.
 struct FewTile {
     int blocks, cols;
     int64_t units, workgroups;
@@ -263,12 +264,13 @@ static int launch_dense(const MxFArgs& f, hipStream_t st) {
 // Grouped: four waves on 16 rows and 32 columns, two of them sharing K (80 packed rows over 17
 // groups, 4096 x 2048: 14.2 us against 16.4 with 16 columns and 15.4 with 64, which need no split),
 // or on 16 columns where 32 would leave compute units without work (4 rows over 4 groups, 1024 x
-// 2048: 3.3 us against 3.8), or on 32 rows and 64 columns, without a split, where the groups have more
-// than about 12 rows (400 packed rows over 17 groups 17.8 us against 23.6; 200 rows 16.4 either way)
-// and there are workgroups for all compute units (1000 rows of x, 4096 x 128 over 16 groups 12.8
-// against 23.5, 200 packed rows, 2048 x 256 over 8 groups, 480 of them, 4.6 against 4.9; but 100 of 1024
-// x 2048 over 8 groups, 192 of them, 6.7 against 5.8, 400 of x, 512 x 384 over 30, 344, 5.8 against 5.1).
-// The rule is the same for A packed and x, so that both add their sums in the same order.
+// 2048: 3.3 us against 3.8), or on 32 rows and 64 columns, without a split, where the groups have
+// more than about 12 rows (400 packed rows over 17 groups 17.8 us against 23.6; 200 rows 16.4
+// either way) and there are workgroups for all compute units (1000 rows of x, 4096 x 128 over 16
+// groups 12.8 against 23.5, 200 packed rows, 2048 x 256 over 8 groups, 480 of them, 4.6 against
+// 4.9; but 100 of 1024 x 2048 over 8 groups, 192 of them, 6.7 against 5.8, 400 of x, 512 x 384 over
+// 30, 344, 5.8 against 5.1). The rule is the same for A packed and x, so that both add their sums
+// in the same order.
 template <typename T, typename XT>
 static int launch_rows(const MxFArgs& f, hipStream_t st) {
     // every group, and the rows in none, may end in a partial unit

@@ -10,25 +10,29 @@
 
 namespace nvfp4 {
 
-// How C is stored.  bfloat16 streams past the caches (grouped 16384 x 4096 x 2048 95 us against 100
-// with ordinary stores; with a quantizer reading C back 8192 x 9216 x 4096 186 against 182, 2048 x
-// 4096 x 2048 the same).  float32 does where C is larger than the last-level cache (256 MB), so
-// that no reader could find much of it there: 15 gradients of 4096 x 2048 (503 MB) 109 us against
-// 141, 8192 x 9216 x 4096 (302 MB) with its reader 227 against 242; but 268 MB (8192 x 8192 x 2048)
-// with a reader 157 against 145, 134 MB 109 against 100.  Gradients of groups are read after the
-// whole backward pass: they do from half of that on, which leaves the cache to the next layer's
-// operands (15 of 1536 x 2048, 189 MB: 43 us either way, a step of their layer 164 against 187).
+// How C is stored.  bfloat16 always streams past the caches: where no kernel reads C next that
+// gains (grouped 16384 x 4096 x 2048 95 us against 100 with ordinary stores), where a quantizer
+// does it loses less (8192 x 9216 x 4096 with its reader 186 against 182, 2048 x 4096 x 2048 the
+// same), and the call does not know which.  float32 does where C is larger than the last-level
+// cache (256 MB), so that no reader could find much of it there: 15 gradients of 4096 x 2048 (503
+// MB) 109 us against 141, 8192 x 9216 x 4096 (302 MB) with its reader 227 against 242; but 268 MB
+// (8192 x 8192 x 2048) with a reader 157 against 145, 134 MB 109 against 100.  Gradients of groups
+// are read after the whole backward pass: they do from half of that on, which leaves the cache to
+// the next layer's operands (measured at one size, 15 of 1536 x 2048, 189 MB: 43 us either way, a
+// step of their layer 164 against 187).  A dense float32 C may be Y or dX, which are read next: it
+// keeps the upper bound.
 static bool streams(const MxGArgs& g, int mode) {
     return mode == MxK ? g.M * g.N * 4 * g.n_groups > ((int64_t)128 << 20) : g.M * g.N * 4 > ((int64_t)256 << 20);
 }
 
-// Which tile.  256 x 256 tiles run one to a compute unit, 256 at a time; 128 x 128 tiles two to a
-// unit.  In percent of a round of the large ones, 512 small ones take 68 and up to 256 of them 45
-// (8192^3: 4 rounds 232 us against 8 299 us; 2048 x 2048 x 4096: 64 large 25.1 us, 256 small 12.5),
-// so the small tile wins where the large ones' last round would be mostly empty: 2048 x 9216 x 4096
-// (288 large tiles) 49 against 56 us, 1024 x 6144 x 4096 (96) 19.6 against 24.9, but 1024 x 9216 x
-// 4096 (144 large, 576 small) 30.3 against 25.8.  Groups of rows end in half a tile on average:
-// 2048 rows over 29 groups (x 4096 x 2048) 27.6 against 36.3, 16384 rows 105.7 against 95.7.
+// Which tile.  256 x 256 tiles run one to a compute unit, 256 at a time (these rules count
+// workgroups for an MI355X's 256 units); 128 x 128 tiles two to a unit.  In percent of a round of
+// the large ones, 512 small ones take 68 and up to 256 of them 45 (8192^3: 4 rounds 232 us against
+// 8 299 us; 2048 x 2048 x 4096: 64 large 25.1 us, 256 small 12.5), so the small tile wins where the
+// large ones' last round would be mostly empty: 2048 x 9216 x 4096 (288 large tiles) 49 against 56
+// us, 1024 x 6144 x 4096 (96) 19.6 against 24.9, but 1024 x 9216 x 4096 (144 large, 576 small) 30.3
+// against 25.8.  Groups of rows end in half a tile on average: 2048 rows over 29 groups (x 4096 x
+// 2048) 27.6 against 36.3, 16384 rows 105.7 against 95.7.
 template <int MODE>
 static int launch_gemm(const MxGArgs& g, int c_dtype, hipStream_t st) {
     const auto tiles = [&](int64_t side) {
@@ -119,15 +123,15 @@ static size_t linear_code_bytes(int64_t M, int64_t K) {
 
 // Few rows are quantized inside the product, which saves a launch (about 3 us) and the workspace,
 // as long as every workgroup's doing so costs less.  Dense: a workgroup's elements times the
-// workgroups a compute unit, up to 48 Ki.  64 x 1024 x 2048 (32 Ki) 5.6 us of GPU time against 6.4 as
-// two kernels, 32 x 4096 x 1024 (32 Ki) 6.0 against 6.5, 12 x 4096 x 4096 (48 Ki) 7.0
-// against 6.9 and a launch less; 32 x 1024 x 4096 (64 Ki) 8.2 against 7.0, 16 x 9216 x 2048 (72 Ki)
-// 10.0 against 7.6.  One or two rows cost less than the launch whatever their length: 1 x 50000 x
-// 4096 20.2 against 23.2, 2 x 21.5 against 23.3, 4 x 26.4 against 23.7.  Grouped: up to 8 Ki elements,
-// or a row, a group.  Of N x K 4096 x 2048 and 17 groups 40 rows (5 Ki a group) 16.2 against 17.0, 60
-// rows (7 Ki) 18.0 against 17.3; of 1536 x 2048 and 29 groups 64 rows 12.0 against 13.3, 128 rows (9
-// Ki) 15.4 against 14.2; of 9216 x 4096 and 4 groups 8 rows 16.0 against 18.2, 16 rows (16 Ki) 21.4
-// against 19.4.
+// workgroups a compute unit, up to 48 Ki.  64 x 1024 x 2048 (32 Ki) 5.6 us of GPU time against 6.4
+// as two kernels, 32 x 4096 x 1024 (32 Ki) 6.0 against 6.5, 12 x 4096 x 4096 (48 Ki) 7.0 against
+// 6.9 and a launch less; 32 x 1024 x 4096 (64 Ki) 8.2 against 7.0, 16 x 9216 x 2048 (72 Ki) 10.0
+// against 7.6.  One or two rows cost less than the launch whatever their length: 1 x 50000 x 4096
+// 20.2 against 23.2, 2 x 21.5 against 23.3, 4 x 26.4 against 23.7.  Grouped: up to 8 Ki elements,
+// or a row, a group.  Of N x K 4096 x 2048 and 17 groups 40 rows (5 Ki a group) 16.2 against 17.0,
+// 60 rows (7 Ki) 18.0 against 17.3 and a launch less; of 1536 x 2048 and 29 groups 64 rows 12.0
+// against 13.3, 128 rows (9 Ki) 15.4 against 14.2; of 9216 x 4096 and 4 groups 8 rows 16.0 against
+// 18.2, 16 rows (16 Ki) 21.4 against 19.4.
 static bool linear_fused(int64_t M, int64_t N, int64_t K, int64_t n_groups) {
     const int64_t kp = mx_pad(K), busy = n_groups < M ? n_groups : M;
     if (M <= 0 || K <= 0) return false;

@@ -6,6 +6,11 @@
 //
 // Bound by memory: an element costs 2 or 4 bytes read and 17/32 written per copy.  There is no
 // pass for a tensor maximum, so every element is read once.
+//
+// Stochastic rounding of bfloat16 is bound by the vector units instead (busy in 0.84 of the
+// cycles, in 0.42 to nearest): ten Philox rounds per eight elements and copy, and a conversion
+// each.  8192 x 9216 both copies 78 us against 47 to nearest, the row copy alone 44 against 35;
+// 8192 x 4608 float32 both 52 against 45; 8191 x 1536 bfloat16 in 15 groups 25 against 15.
 #include "mx_common.h"
 
 namespace nvfp4 {
@@ -55,8 +60,8 @@ __device__ __forceinline__ uint32_t codes_of(const Oct<T>& o, uint32_t code, boo
 // Rowwise copy alone: a lane per eight elements, a quad per block, so that loads and stores
 // are contiguous over the wave.  A workgroup takes kRowSteps times 256 consecutive octs of the
 // copy (rows padded to row_kp), all loaded before the first is used.  From memory (inputs of 600 MB
-// in turn) 8192 x 9216 bfloat16 37 us, 5.2 TB/s read and written; 16 x 4096 2.7 us, an empty kernel's
-// time.
+// in turn) 8192 x 9216 bfloat16 35 to 37 us, 5.5 to 5.2 TB/s read and written; 16 x 4096 2.7 us, an
+// empty kernel's time.
 constexpr int kRowSteps = 4;
 template <typename T, bool SR>
 __global__ __launch_bounds__(256) void k_mx_rows(MxQArgs g) {
@@ -91,7 +96,7 @@ __global__ __launch_bounds__(256) void k_mx_rows(MxQArgs g) {
 // bfloat16 columns or one float32 one) of 32 rows.  Dword c of row r lies at c ^ 16 (r / 32), so
 // that the four row blocks of 16 dword columns, which a wave reads at once (a quad of lanes
 // per column, for 64 contiguous bytes of its codes), are in different banks.  From memory 8192 x 9216
-// bfloat16 49 us, 4.7 TB/s; 8192 x 4608 float32 47 us, 4.0 TB/s.
+// bfloat16 47 to 49 us, 4.9 to 4.7 TB/s; 8192 x 4608 float32 45 to 47 us, 4.2 to 4.0 TB/s.
 template <typename T, bool SR>
 __global__ __launch_bounds__(256) void k_mx_tile(MxQArgs g, unsigned units, unsigned col_tiles) {
     constexpr int kTileCols = 256 / sizeof(T), kPerRow = kTileCols / 8;   // octs of a tile row

@@ -282,10 +282,10 @@ def mxfp4_quant_params(rowwise=True, colwise=False, scale_rule=MXFP4_SCALE_FLOOR
 
 
 def mxfp4_quantize(x, params, offsets=None, row_out=None, col_out=None):
-    """Quantize a bf16/fp32 CUDA tensor [rows][cols] or [batch][rows][cols] (any row and batch
-    strides, unit column stride).  Returns (row_copy, col_copy), None for one not requested: the
-    rowwise copy [.., rows][cols] and the columnwise copy [.., cols][rows].  With offsets (2-D x
-    only) the columnwise copy's blocks restart at each group of rows."""
+    """Quantize a bf16/fp32 CUDA tensor [rows][cols] or [batch][rows][cols] (any batch stride, rows
+    that do not overlap, unit column stride).  Returns (row_copy, col_copy), None for one not
+    requested: the rowwise copy [.., rows][cols] and the columnwise copy [.., cols][rows].  With
+    offsets (2-D x only) the columnwise copy's blocks restart at each group of rows."""
     dev, shape, dtype, pitch = _matrix(x, "x")
     if len(shape) > 3:
         raise _error("x must be a 2-D or 3-D tensor")
