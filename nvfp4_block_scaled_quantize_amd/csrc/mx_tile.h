@@ -16,7 +16,8 @@ constexpr uint32_t kBias = 3072;
 // through their code for it.  (Taking M0's content from set_m0 into each load as an operand would let
 // the compiler see that too, but holds one more scalar register: 0.5 to 1 % of the large products.)
 __device__ __forceinline__ void set_m0(uint32_t lds_addr) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0" ::"s"(lds_addr) : "memory", "m0");
+    uint32_t m0;
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0" : "={m0}"(m0) : "s"(lds_addr) : "memory");
 }
 template <int OFFSET>
 __device__ __forceinline__ void dma16_at(int4v rsrc, uint32_t voff, uint32_t soff) {
