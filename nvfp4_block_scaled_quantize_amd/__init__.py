@@ -13,7 +13,8 @@ Entry points (same names as the C ABI):
   qadamw_v_encode    Q-AdamW second-moment encode (sqrt, bf16 tile mean, RHT, NVFP4)
   qadamw_v_decode    its inverse
 The MXFP4 operators (E8M0 scales per 32; dense and grouped-by-expert products) are in
-``mxfp4.py`` and re-exported here.
+``mxfp4.py``, the gated feed-forward block on them and the 8-bit activation checkpoints in
+``mxffn.py``; both are re-exported here.
 """
 import ctypes
 import os
@@ -26,6 +27,10 @@ from . import mxfp4 as _mxfp4
 from .mxfp4 import (MXFP4_SCALE_CEIL, MXFP4_SCALE_FLOOR, MXTensor, mxfp4_dequantize, mxfp4_gemm,
                     mxfp4_gemm_grouped, mxfp4_gemm_grouped_wgrad, mxfp4_linear,
                     mxfp4_linear_workspace_bytes, mxfp4_quant_params, mxfp4_quantize)
+from . import mxffn as _mxffn
+from .mxffn import (MXFP4_GELU, MXFP4_SILU, MX8Tensor, mxfp4_gated, mxfp4_gated_backward, mxfp4_gated_linear,
+                    mxfp4_gated_linear_workspace_bytes, mxfp8_dequantize, mxfp8_gated_backward,
+                    mxfp8_quantize, mxfp8_to_mxfp4)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libnvfp4.so")
@@ -143,10 +148,11 @@ def load_library(path: Optional[str] = None):
     if lib.nvfp4_abi_version() != ABI_VERSION:
         raise Nvfp4Error(f"{p} has ABI version {lib.nvfp4_abi_version()}, this binding expects "
                          f"{ABI_VERSION}: rebuild the HIP library (__graft_entry__.build())")
-    unusable = _mxfp4.bind(lib)
+    unusable, ffn_unusable = _mxfp4.bind(lib), _mxffn.bind(lib)
     if path is None:
         _lib = lib
         _mxfp4.attach(lib, unusable)
+        _mxffn.attach(lib, ffn_unusable)
     return lib
 
 

@@ -11,12 +11,14 @@
 // cycles, in 0.42 to nearest): ten Philox rounds per eight elements and copy, and a conversion
 // each.  8192 x 9216 both copies 78 us against 47 to nearest, the row copy alone 44 against 35;
 // 8192 x 4608 float32 both 52 against 45; 8191 x 1536 bfloat16 in 15 groups 25 against 15.
-#include "mx_common.h"
+#include "mx_ffn.h"
+#include "mx_pieces.h"
 
 namespace nvfp4 {
 
 struct MxQArgs {
     const void* x;
+    const uint8_t* xs;              // x is a checkpoint's codes: their scales
     int64_t batch, rows, cols, ld, stride;
     const int32_t* offsets;
     int n_groups;
@@ -27,6 +29,32 @@ struct MxQArgs {
     int stream;                     // read x past the caches
     uint32_t k0, k1;                // Philox key
 };
+
+// Eight elements of x from element `at` on, of which `left` exist.  FROM8: of a checkpoint, whose rows
+// are whole blocks, rounded to bfloat16 (which changes only values below 2^-126).
+template <bool FROM8, typename T, bool STREAM = false>
+__device__ __forceinline__ Oct<T> load_x(const MxQArgs& g, int64_t at, int64_t left) {
+    if constexpr (!FROM8) return load_oct<T, STREAM>((const T*)g.x + at, left);
+    else {
+        Oct<T> o = {};
+        if (left <= 0) return o;
+        const uint2v* p = (const uint2v*)((const uint8_t*)g.x + at);
+        uint2v w = STREAM ? __builtin_nontemporal_load(p) : *p;
+        const float s = mx8_factor(g.xs[at / kMxBlock]);
+        if (left < 8) {
+            const uint64_t keep = ((uint64_t)1 << (8 * left)) - 1;
+            w[0] &= (uint32_t)keep, w[1] &= (uint32_t)(keep >> 32);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const Quad q = mx8_values(w[i], s);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                o.w[2 * i + j] = __builtin_bit_cast(uint32_t, bf16x2v{(__bf16)q.v[2 * j], (__bf16)q.v[2 * j + 1]});
+        }
+        return o;
+    }
+}
 
 // Stochastic: x / s in binary32 (exact but for results below 2^-126, which round to 0 with
 // every draw that f 2^16 < 1 allows), then the conversion at unit scale.  e: the first
@@ -63,7 +91,7 @@ __device__ __forceinline__ uint32_t codes_of(const Oct<T>& o, uint32_t code, boo
 // in turn) 8192 x 9216 bfloat16 35 to 37 us, 5.5 to 5.2 TB/s read and written; 16 x 4096 2.7 us, an
 // empty kernel's time.
 constexpr int kRowSteps = 4;
-template <typename T, bool SR>
+template <typename T, bool SR, bool FROM8>
 __global__ __launch_bounds__(256) void k_mx_rows(MxQArgs g) {
     const uint32_t per = (uint32_t)(g.row_kp / 8);      // octs of a row
     const int64_t first = (int64_t)blockIdx.x * (256 * kRowSteps), total = g.batch * g.rows * per;
@@ -76,7 +104,7 @@ __global__ __launch_bounds__(256) void k_mx_rows(MxQArgs g) {
         const int64_t r = row0 + dr, k = (int64_t)(at - dr * per) * 8;
         const int64_t b = g.batch == 1 ? 0 : r / g.rows;
         const bool in = first + threadIdx.x + 256 * i < total;
-        o[i] = load_oct((const T*)g.x + b * g.stride + (r - b * g.rows) * g.ld + k, in ? g.cols - k : 0);
+        o[i] = load_x<FROM8, T>(g, b * g.stride + (r - b * g.rows) * g.ld + k, in ? g.cols - k : 0);
     }
 #pragma unroll
     for (int i = 0; i < kRowSteps; ++i) {
@@ -97,7 +125,7 @@ __global__ __launch_bounds__(256) void k_mx_rows(MxQArgs g) {
 // that the four row blocks of 16 dword columns, which a wave reads at once (a quad of lanes
 // per column, for 64 contiguous bytes of its codes), are in different banks.  From memory 8192 x 9216
 // bfloat16 47 to 49 us, 4.9 to 4.7 TB/s; 8192 x 4608 float32 45 to 47 us, 4.2 to 4.0 TB/s.
-template <typename T, bool SR>
+template <typename T, bool SR, bool FROM8>
 __global__ __launch_bounds__(256) void k_mx_tile(MxQArgs g, unsigned units, unsigned col_tiles) {
     constexpr int kTileCols = 256 / sizeof(T), kPerRow = kTileCols / 8;   // octs of a tile row
     constexpr int kRowsAtOnce = 256 / kPerRow, kSteps = kMxPad / kRowsAtOnce;
@@ -120,13 +148,13 @@ __global__ __launch_bounds__(256) void k_mx_tile(MxQArgs g, unsigned units, unsi
     const int64_t c0 = (int64_t)ct * kTileCols;
     const int tr = t / kPerRow, tc = t % kPerRow;        // this lane's row and oct of a step
     const int64_t left = g.cols - c0 - tc * 8;
-    const T* p = (const T*)g.x + b * g.stride + (row0 + tr) * g.ld + c0 + tc * 8;
+    const int64_t first = b * g.stride + (row0 + tr) * g.ld + c0 + tc * 8;
     Oct<T> o[kSteps];
     const auto load = [&](auto stream) {
 #pragma unroll
         for (int i = 0; i < kSteps; ++i)
-            o[i] = load_oct<T, decltype(stream)::value>(p + (int64_t)i * kRowsAtOnce * g.ld,
-                                                        tr + i * kRowsAtOnce < rows ? left : 0);
+            o[i] = load_x<FROM8, T, decltype(stream)::value>(g, first + (int64_t)i * kRowsAtOnce * g.ld,
+                                                             tr + i * kRowsAtOnce < rows ? left : 0);
     };
     if (g.stream) load(std::true_type{});
     else load(std::false_type{});
@@ -217,11 +245,6 @@ struct MxDArgs {
     int64_t ld;
 };
 
-// The decode's piece of a lane: 16 bytes of output, so that a wave's stores are contiguous.
-template <typename T> struct Piece;
-template <> struct Piece<uint16_t> { static constexpr int n = 8; using Codes = uint32_t; };
-template <> struct Piece<float> { static constexpr int n = 4; using Codes = uint16_t; };
-
 // A lane's decoded elements as four dwords.  bfloat16: exact for copies of bfloat16 values,
 // nearest even otherwise.
 template <typename T>
@@ -239,45 +262,6 @@ __device__ __forceinline__ int4v decode_piece(uint32_t w, uint32_t code) {
     int4v d;
     __builtin_memcpy(&d, e, sizeof(d));
     return d;
-}
-
-// Dword-aligned vectors, stored past the caches: 8192 x 9216 bfloat16 28 us against 38 with
-// ordinary stores, and 60 against 66 together with a quantizer that reads them back.
-typedef int int3a __attribute__((ext_vector_type(3), aligned(4)));
-
-// Stores the piece d at p, of which `left` elements lie in the row (<= 0: none).  Lanes of a
-// wave hold consecutive pieces; `first`: the previous lane's is not the one before this in its
-// row.  Where p is an odd bfloat16, the lane stores the dwords that its piece ends, taking the
-// previous lane's last element, so that rows of any pitch are written in dwords: 4096 x 8191
-// bfloat16 16 us against 22 with 16-byte stores at odd addresses.  All 64 lanes call.
-template <typename T>
-__device__ __forceinline__ void store_piece(int4v d, T* p, int64_t left, bool first) {
-    constexpr int n = Piece<T>::n;
-    if constexpr (sizeof(T) == 2) {
-        const int before = dpp<kWaveShr1>(0, d[3]);
-        if (((uintptr_t)p & 2) && left >= n) {
-            const int4v o = {(int)__builtin_amdgcn_alignbit(d[0], before, 16), (int)__builtin_amdgcn_alignbit(d[1], d[0], 16),
-                             (int)__builtin_amdgcn_alignbit(d[2], d[1], 16), (int)__builtin_amdgcn_alignbit(d[3], d[2], 16)};
-            if (first) {
-                *p = (T)d[0];
-                __builtin_nontemporal_store((int3a){o[1], o[2], o[3]}, (int3a*)(p + 1));
-            } else {
-                __builtin_nontemporal_store((int4_by4)o, (int4_by4*)(p - 1));
-            }
-            // no whole piece after this one in the wave: nobody else stores the last element
-            if (left < 2 * n || (threadIdx.x & 63) == 63) p[n - 1] = (T)((uint32_t)d[3] >> 16);
-            return;
-        }
-    }
-    if (left >= n) {
-        __builtin_nontemporal_store((int4_by4)d, (int4_by4*)p);
-        return;
-    }
-    T e[n];
-    __builtin_memcpy(e, &d, sizeof(e));
-#pragma unroll
-    for (int i = 0; i < n; ++i)
-        if (i < left) p[i] = e[i];
 }
 
 // Plain copy: consecutive pieces of the padded copy, as k_mx_rows.
@@ -370,23 +354,51 @@ static int launch_decode(const MxDArgs& g, hipStream_t st) {
     return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
 }
 
-template <typename T, bool SR>
+template <typename T, bool SR, bool FROM8 = false>
 static int launch_quantize(const MxQArgs& g, hipStream_t st) {
     if (!g.cc) {
         const int per = 256 * kRowSteps;
         const __int128 grid = ((__int128)g.batch * g.rows * (g.row_kp / 8) + per - 1) / per;
         if (!mx_grid_fits(grid, 256)) return NVFP4_ERR_SHAPE;
-        k_mx_rows<T, SR><<<dim3((unsigned)grid), 256, 0, st>>>(g);
+        k_mx_rows<T, SR, FROM8><<<dim3((unsigned)grid), 256, 0, st>>>(g);
     } else {
         // units cover the rows in no group too (one more partial unit at most); tiles cover the
         // rowwise copy's padding
         const int64_t units = g.col_kp / kMxPad, col_tiles = g.row_kp * (int64_t)sizeof(T) / 256;
         const __int128 grid = (g.n_groups ? units + 1 : (__int128)units * g.batch) * col_tiles;
         if (!mx_grid_fits(grid, 256)) return NVFP4_ERR_SHAPE;
-        k_mx_tile<T, SR><<<dim3((unsigned)grid), 256, 0, st>>>(g, (unsigned)units, (unsigned)col_tiles);
+        k_mx_tile<T, SR, FROM8><<<dim3((unsigned)grid), 256, 0, st>>>(g, (unsigned)units, (unsigned)col_tiles);
     }
     return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
 }
+
+// The arguments that mxfp4_quantize and mxfp8_to_mxfp4 share.  *used: there is anything to do.
+static int check_copies(MxQArgs& g, int64_t batch, int64_t rows, int64_t cols, const int32_t* offsets, int64_t n_groups,
+                        const mxfp4_quant_params* p, const mxfp4_tensor* row_out, const mxfp4_tensor* col_out,
+                        bool* used) {
+    const auto flag = [](int32_t v) { return v == 0 || v == 1; };
+    if (!flag(p->rowwise) || !flag(p->colwise) || !(p->rowwise || p->colwise) || !flag(p->scale_rule) ||
+        !flag(p->round_row) || !flag(p->round_col))
+        return NVFP4_ERR_MODE;
+    if (int rc = mx_check_groups(offsets, n_groups, rows)) return rc;
+    if (n_groups && batch != 1) return NVFP4_ERR_MODE;
+    *used = batch && rows && cols;
+    if (p->rowwise)
+        if (int rc = mx_check_tensor(row_out, *used)) return rc;
+    if (p->colwise)
+        if (int rc = mx_check_tensor(col_out, *used)) return rc;
+    g.row_kp = mx_pad(cols);
+    g.col_kp = n_groups ? mxfp4_grouped_k(rows, n_groups) : mx_pad(rows);
+    g.batch = batch, g.rows = rows, g.cols = cols;
+    g.offsets = offsets, g.n_groups = (int)n_groups;
+    if (p->rowwise) g.rc = row_out->codes, g.rs = row_out->scales;
+    if (p->colwise) g.cc = col_out->codes, g.cs = col_out->scales;
+    g.k0 = (uint32_t)p->seed, g.k1 = (uint32_t)(p->seed >> 32);
+    g.above = mx_above(p->scale_rule);
+    g.sr_row = p->round_row == NVFP4_SR, g.sr_col = p->round_col == NVFP4_SR;
+    return NVFP4_OK;
+}
+static bool stochastic(const MxQArgs& g) { return (g.rc && g.sr_row) || (g.cc && g.sr_col); }
 
 }  // namespace nvfp4
 
@@ -410,38 +422,38 @@ extern "C" int mxfp4_quantize(const void* x, int dtype, int64_t batch, int64_t r
     if (!mx_extent(batch) || !mx_extent(rows) || !mx_extent(cols) || ld_x < cols) return NVFP4_ERR_SHAPE;
     const int size = mx_dtype_size(dtype);
     if (!size) return NVFP4_ERR_DTYPE;
-    const auto flag = [](int32_t v) { return v == 0 || v == 1; };
-    if (!flag(p->rowwise) || !flag(p->colwise) || !(p->rowwise || p->colwise) || !flag(p->scale_rule) ||
-        !flag(p->round_row) || !flag(p->round_col))
-        return NVFP4_ERR_MODE;
-    if (int rc = mx_check_groups(offsets, n_groups, rows)) return rc;
-    if (n_groups && batch != 1) return NVFP4_ERR_MODE;
-    const bool used = batch && rows && cols;
-    if (p->rowwise)
-        if (int rc = mx_check_tensor(row_out, used)) return rc;
-    if (p->colwise)
-        if (int rc = mx_check_tensor(col_out, used)) return rc;
     MxQArgs g = {};
-    g.row_kp = mx_pad(cols);
-    g.col_kp = n_groups ? mxfp4_grouped_k(rows, n_groups) : mx_pad(rows);
+    bool used;
+    if (int rc = check_copies(g, batch, rows, cols, offsets, n_groups, p, row_out, col_out, &used)) return rc;
     if (!used) return NVFP4_OK;
     if (!x) return NVFP4_ERR_NULL;
     if ((uintptr_t)x % size) return NVFP4_ERR_ALIGN;
-    g.x = x, g.batch = batch, g.rows = rows, g.cols = cols, g.ld = ld_x, g.stride = batch_stride;
-    g.offsets = offsets, g.n_groups = (int)n_groups;
-    if (p->rowwise) g.rc = row_out->codes, g.rs = row_out->scales;
-    if (p->colwise) g.cc = col_out->codes, g.cs = col_out->scales;
-    g.k0 = (uint32_t)p->seed, g.k1 = (uint32_t)(p->seed >> 32);
+    g.x = x, g.ld = ld_x, g.stride = batch_stride;
     const hipStream_t st = (hipStream_t)stream;
-    g.above = mx_above(p->scale_rule);
-    g.sr_row = p->round_row == NVFP4_SR, g.sr_col = p->round_col == NVFP4_SR;
     // An input of half the last-level cache (256 MB) or more is not still there from its
     // producer, whose own operands went through as well: past the caches 8192 x 9216 bfloat16
     // takes 50 us against 58 when it comes from memory, but 47 against 39 when it is cached.
     g.stream = (__int128)batch * rows * cols * size >= ((int64_t)128 << 20);
-    const bool sr = (g.rc && g.sr_row) || (g.cc && g.sr_col);
+    const bool sr = stochastic(g);
     if (dtype == NVFP4_BF16) return sr ? launch_quantize<uint16_t, true>(g, st) : launch_quantize<uint16_t, false>(g, st);
     return sr ? launch_quantize<float, true>(g, st) : launch_quantize<float, false>(g, st);
+}
+
+extern "C" int mxfp8_to_mxfp4(const mxfp8_tensor* q, int64_t batch, int64_t rows, int64_t cols, const int32_t* offsets,
+                              int64_t n_groups, const mxfp4_quant_params* p, const mxfp4_tensor* row_out,
+                              const mxfp4_tensor* col_out, void* stream) {
+    if (!p) return NVFP4_ERR_NULL;
+    if (!mx_extent(batch) || !mx_extent(rows) || !mx_extent(cols)) return NVFP4_ERR_SHAPE;
+    MxQArgs g = {};
+    bool used;
+    if (int rc = check_copies(g, batch, rows, cols, offsets, n_groups, p, row_out, col_out, &used)) return rc;
+    if (int rc = mx8_check_tensor(q, used)) return rc;
+    if (!used) return NVFP4_OK;
+    g.x = q->codes, g.xs = q->scales, g.ld = mx_pad(cols);
+    g.stride = (int64_t)((uint64_t)rows * (uint64_t)g.ld);      // (a product past 64 bits is refused with the grid)
+    g.stream = (__int128)batch * rows * g.ld >= ((int64_t)128 << 20);       // as in mxfp4_quantize
+    const hipStream_t st = (hipStream_t)stream;
+    return stochastic(g) ? launch_quantize<uint16_t, true, true>(g, st) : launch_quantize<uint16_t, false, true>(g, st);
 }
 
 extern "C" int mxfp4_dequantize(const mxfp4_tensor* q, int64_t n, int64_t k, const int32_t* offsets,
