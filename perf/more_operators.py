@@ -355,8 +355,10 @@ def _library(s):
     if not case["out"]:
         return list(nv.mxfp8_gated_backward(s["dh"], kept, activation=act, h=True))
     dy, _ = nv.mxfp4_quantize(s["dy"], p)
-    return list(nv.mxfp4_gated_backward(dy, nv.MXTensor(*s["w2"], case["out"]), kept, offsets=offsets,
-                                        activation=act, out_dtype=dtype, h=True))
+    if "w2_copy" not in s:      # the calls take contiguous copies: the layer's weights are laid out once
+        s["w2_copy"] = nv.MXTensor(*(t.contiguous() for t in s["w2"]), case["out"])
+    return list(nv.mxfp4_gated_backward(dy, s["w2_copy"], kept, offsets=offsets, activation=act,
+                                        out_dtype=dtype, h=True))
 
 
 def run(state):
