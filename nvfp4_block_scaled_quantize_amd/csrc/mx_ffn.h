@@ -78,35 +78,6 @@ struct MxFfnArgs {
 };
 
 typedef uint32_t uint2v __attribute__((ext_vector_type(2)));
-typedef int int2_by2 __attribute__((ext_vector_type(2), aligned(2)));
-typedef int int4_by4f __attribute__((ext_vector_type(4), aligned(4)));
-// Four consecutive elements of a row, of which `left` exist.
-__device__ __forceinline__ void store_c4(uint16_t* p, float a, float b, float c, float d, int left) {
-    alignas(8) uint16_t e[4];
-    put_c4(e, a, b, c, d);
-    if (left >= 4) {
-        int2_by2 v;
-        __builtin_memcpy(&v, e, 8);
-        *(int2_by2*)p = v;
-    } else {
-#pragma unroll
-        for (int i = 0; i < 3; ++i)
-            if (i < left) p[i] = e[i];
-    }
-}
-__device__ __forceinline__ void store_c4(float* p, float a, float b, float c, float d, int left) {
-    const float e[4] = {a, b, c, d};
-    if (left >= 4) {
-        int4_by4f v;
-        __builtin_memcpy(&v, e, 16);
-        *(int4_by4f*)p = v;
-    } else {
-#pragma unroll
-        for (int i = 0; i < 3; ++i)
-            if (i < left) p[i] = e[i];
-    }
-}
-
 // The upper half of a's lanes and the lower half of b's change places.
 __device__ __forceinline__ void swap_halves(uint32_t& a, uint32_t& b) {
     const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
@@ -171,66 +142,192 @@ __device__ __forceinline__ void spread_checkpoint(uint4 v, uint32_t (&d)[4]) {
     swap_halves(d[1], d[3]);
 }
 
-// The forward's results from a block of G and of U: row m of the lane (stored if `in`), columns from
-// c0, of which `left` are below N (the rest are zeros in the copies).
-template <typename T, int ACT>
-__device__ __forceinline__ void put_forward(const MxFfnArgs& f, float16v& g, float16v& u, int64_t m, bool in, int64_t c0,
-                                            int left, int h) {
-    float16v x;
+// What a tiled kernel's product is for: C itself, the block's forward, or its backward.
+// (Constants and a trait with a name each: what is unnamed would be part of the kernels' names.)
+constexpr int kProduct = 0, kForward = 1, kBackward = 2;
+template <int KIND> struct MxKind { using Args = MxFfnArgs; };
+template <> struct MxKind<kProduct> { using Args = MxGArgs; };
+template <int KIND> using MxKindArgs = typename MxKind<KIND>::Args;
+__host__ __device__ inline const MxGArgs& mx_product(const MxGArgs& a) { return a; }
+__host__ __device__ inline const MxGArgs& mx_product(const MxFfnArgs& a) { return a.g; }
+// Rows of a matrix of B for each column of the result.
+template <int KIND> constexpr int kMxWeights = KIND == kForward ? 2 : 1;
+
+// 32 rows x 32 J columns of a result, as blocks of accumulators, to p by way of LDS: `piece`, this wave's 4
+// KiB, takes up to 128 bytes a row, its 16-byte chunks in an order by which eight consecutive rows (or four
+// pairs of them) touch every bank once, and a wave stores whole pieces of rows from there, 16 bytes a lane, past
+// the caches.  `whole`: all rows and columns exist, else `rows` and `left` of them.
+template <typename T, int J>
+__device__ __forceinline__ void put_rows(uint8_t* piece, const float16v (&x)[J], T* p, int64_t ld, int rows, int left,
+                                         bool whole, int lane) {
+    constexpr int kBytes = 32 * J * (int)sizeof(T) < 128 ? 32 * J * (int)sizeof(T) : 128;   // of a row at a time
+    constexpr int kN = kBytes / (int)sizeof(T), kChunks = kBytes / 16, kRows = 64 / kChunks;
+    using Vec = typename Oct<T>::Vec;
+    const auto swizzle = [](int r) { return kChunks == 8 ? r & 7 : (r >> 1) & 3; };
+    int h = lane >> 5, lr = lane & 31, rr = lane / kChunks, q = lane % kChunks;
+    asm volatile("" : "+v"(h), "+v"(lr), "+v"(rr), "+v"(q));    // opaque: addresses are made where they are used
+    const uint8_t* from = piece + rr * kBytes + ((q ^ swizzle(rr)) << 4);
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-        if (left < 32 && 8 * (r / 4) + 4 * h + r % 4 >= left) g[r] = u[r] = 0.0f;
-        x[r] = act_value<ACT>(g[r]) * u[r];
-    }
-    if (f.g.c && in) {
-        T* p = (T*)f.g.c + m * f.g.ldc + c0 + 4 * h;
+    for (int pass = 0; pass < 32 * J / kN; ++pass) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-            store_c4(p + 8 * q, x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3], left - 8 * q - 4 * h);
-    }
-    const int64_t at = m * f.np + c0;
-    if (f.qc) put_copy_block(x, f.above, f.qc + at / 2, f.qs + at / 32, h, in);
-    if (f.kc) {
-        const int64_t second = f.g.M * f.np;
-        put_checkpoint_block(g, f.kc + at, f.ks + at / 32, h, in);
-        put_checkpoint_block(u, f.kc + second + at, f.ks + (second + at) / 32, h, in);
+        for (int j = 0; j < kN / 32; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; r += 4) {
+                const int byte = (j * 32 + 2 * r + 4 * h) * (int)sizeof(T);
+                const float16v& v = x[pass * (kN / 32) + j];
+                put_c4((T*)(piece + lr * kBytes + (((byte >> 4) ^ swizzle(lr)) << 4) + (byte & 15)), v[r], v[r + 1], v[r + 2],
+                       v[r + 3]);
+            }
+        const int col = pass * kN + q * (16 / (int)sizeof(T));
+        T* to = p + rr * ld + col;
+        if (whole) {
+#pragma unroll
+            for (int k = 0; k < 32 / kRows; ++k) {
+                __builtin_nontemporal_store((Vec)*(const int4v*)(from + k * 1024), (Vec*)to);
+                to += kRows * ld;
+            }
+        } else {
+#pragma unroll 1
+            for (int k = 0; k < 32 / kRows; ++k) {
+                const int4v v = *(const int4v*)(from + k * 1024);
+                if (rr + k * kRows < rows) store_c16<true>(to, v, left - col);
+                to += kRows * ld;
+            }
+        }
     }
 }
 
-// The backward's results from a block d of dH and the checkpoint.  `left` of its columns are below N.
-template <typename T, int ACT>
-__device__ __forceinline__ void put_backward(const MxFfnArgs& f, const float16v& d, int64_t m, bool in, int64_t c0, int left,
-                                             int h, bool zero) {
-    if (!in || left <= 0) return;       // (the same for both lanes of a row)
-    const int64_t at = m * f.np + c0, second = f.g.M * f.np;
-    uint32_t gw[4], uw[4];
-    spread_checkpoint(*(const uint4*)(f.kc + at + 16 * h), gw);
-    spread_checkpoint(*(const uint4*)(f.kc + second + at + 16 * h), uw);
-    const float gs = mx8_factor(f.ks[at / 32]), us = mx8_factor(f.ks[(second + at) / 32]);
-    T* const pg = (T*)f.g.c + m * f.g.ldc + c0 + 4 * h;
-    T* const ph = (T*)f.h + m * f.ldh + c0 + 4 * h;
+// The forward's results from J blocks of G and as many of U: rows from m0, of which `rows` exist, columns from
+// c0, of which `left` are below N (the rest are zeros in the copies, whose rows reach to np).
+template <typename T, int ACT, int J>
+__device__ __forceinline__ void forward_rows(const MxFfnArgs& f, float16v (&g)[J], float16v (&u)[J], uint8_t* piece, int64_t m0,
+                                             int rows, int64_t c0, int left, bool whole, int lane) {
+    const int h = lane >> 5, li = lane & 31;
+    float16v x[J];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const Quad g = mx8_values(gw[q], gs), u = mx8_values(uw[q], us);
-        Quad dg, du, x;
+    for (int j = 0; j < J; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const Act a = act_both<ACT>(g.v[i]);
-            du.v[i] = zero ? 0.0f : d[4 * q + i] * a.a;
-            dg.v[i] = zero ? 0.0f : d[4 * q + i] * u.v[i] * a.slope;
-            x.v[i] = zero ? 0.0f : a.a * u.v[i];
+        for (int r = 0; r < 16; ++r) {
+            if (!whole && 32 * j + 8 * (r / 4) + 4 * h + r % 4 >= left) g[j][r] = u[j][r] = 0.0f;
+            x[j][r] = act_value<ACT>(g[j][r]) * u[j][r];
         }
-        const int n = left - 8 * q - 4 * h;
-        store_c4(pg + 8 * q, dg.v[0], dg.v[1], dg.v[2], dg.v[3], n);
-        store_c4(pg + f.g.N + 8 * q, du.v[0], du.v[1], du.v[2], du.v[3], n);
-        if (f.h) store_c4(ph + 8 * q, x.v[0], x.v[1], x.v[2], x.v[3], n);
+    if (f.g.c) put_rows<T, J>(piece, x, (T*)f.g.c + m0 * f.g.ldc + c0, f.g.ldc, rows, left, whole, lane);
+    if (!f.qc && !f.kc) return;
+    const int64_t at = (m0 + li) * f.np + c0, second = f.g.M * f.np;
+    const bool in = li < rows && c0 < f.np;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+        const int64_t b = at + 32 * j;
+        if (f.qc) put_copy_block(x[j], f.above, f.qc + b / 2, f.qs + b / 32, h, in);
+        if (f.kc) {
+            put_checkpoint_block(g[j], f.kc + b, f.ks + b / 32, h, in);
+            put_checkpoint_block(u[j], f.kc + second + b, f.ks + (second + b) / 32, h, in);
+        }
     }
+}
+// The stores at least that a wave issues for `groups` times 32 whole rows of J blocks: 128 bytes x 8 rows of a
+// tensor each, one a block of the copy's codes, and two of the checkpoint's.
+template <typename T>
+__device__ __forceinline__ int forward_stores(const MxFfnArgs& f, int groups, int blocks) {
+    return groups * blocks * ((f.g.c ? (int)sizeof(T) : 0) + (f.qc ? 1 : 0) + (f.kc ? 2 : 0));
+}
+
+// J blocks of the checkpoint in a row: its 16 J code bytes of G and of U that this lane decodes, and the scales.
+template <int J>
+struct Kept {
+    uint4 g[J], u[J];
+    uint32_t gs, us;
+};
+// Of row m (or the last there is), columns from c0, a multiple of 32 J.  No branch but one that is the same
+// for the whole wave: a join would wait for the loads.
+template <int J>
+__device__ __forceinline__ Kept<J> load_kept(const MxFfnArgs& f, int64_t m, int64_t c0, int h) {
+    using Scales = std::conditional_t<J == 4, uint32_t, uint16_t>;
+    static_assert(J == 4 || J == 2);
+    c0 = c0 < f.np ? c0 : 0;        // (nothing of it will be stored)
+    const int64_t at = (m < f.g.M ? m : f.g.M - 1) * f.np + c0, second = f.g.M * f.np;
+    Kept<J> k;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+        k.g[j] = *(const uint4*)(f.kc + at + 32 * j + 16 * h);
+        k.u[j] = *(const uint4*)(f.kc + second + at + 32 * j + 16 * h);
+    }
+    k.gs = *(const Scales*)(f.ks + at / 32);
+    k.us = *(const Scales*)(f.ks + (second + at) / 32);
+    return k;
+}
+
+// The backward's results from J blocks d of dH and the checkpoint's.
+template <typename T, int ACT, int J>
+__device__ __forceinline__ void backward_rows(const MxFfnArgs& f, const float16v (&d)[J], const Kept<J>& kept, uint8_t* piece,
+                                              int64_t m0, int rows, int64_t c0, int left, bool whole, int lane) {
+    T* const pg = (T*)f.g.c + m0 * f.g.ldc + c0;
+    T* const ph = (T*)f.h + m0 * f.ldh + c0;
+#pragma unroll
+    for (int p = 0; p < J; p += 2) {
+        float16v dg[2], du[2], x[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            uint32_t gw[4], uw[4];
+            spread_checkpoint(kept.g[p + j], gw);
+            spread_checkpoint(kept.u[p + j], uw);
+            const float gs = mx8_factor((kept.gs >> (8 * (p + j))) & 0xFFu), us = mx8_factor((kept.us >> (8 * (p + j))) & 0xFFu);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const Quad g = mx8_values(gw[q], gs), u = mx8_values(uw[q], us);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const Act a = act_both<ACT>(g.v[i]);
+                    const float v = d[p + j][4 * q + i];
+                    du[j][4 * q + i] = v * a.a;
+                    dg[j][4 * q + i] = v * u.v[i] * a.slope;
+                    x[j][4 * q + i] = a.a * u.v[i];
+                }
+            }
+        }
+        put_rows<T, 2>(piece, dg, pg + 32 * p, f.g.ldc, rows, left - 32 * p, whole, lane);
+        put_rows<T, 2>(piece, du, pg + f.g.N + 32 * p, f.g.ldc, rows, left - 32 * p, whole, lane);
+        if (f.h) put_rows<T, 2>(piece, x, ph + 32 * p, f.ldh, rows, left - 32 * p, whole, lane);
+    }
+}
+
+// The results of `rows` rows in no group, `width` columns from n0, by a workgroup of 256.
+template <typename T>
+__device__ __forceinline__ void zero_forward(const MxFfnArgs& f, int64_t m0, int rows, int64_t n0, int width, int t) {
+    const int wid = __builtin_amdgcn_readfirstlane(t >> 6), lane = t & 63;
+    const int64_t second = f.g.M * f.np;
+    for (int r = wid; r < rows; r += 4) {
+        const int64_t m = m0 + r, at = m * f.np + n0;
+        if (f.g.c)
+            for (int k = lane; k < width && n0 + k < f.g.N; k += 64) store_c((T*)f.g.c + m * f.g.ldc + n0 + k, 0.0f);
+        if (n0 >= f.np) continue;
+        if (f.qc && lane < width / 32) *(uint4*)(f.qc + at / 2 + 16 * lane) = uint4{}, f.qs[at / 32 + lane] = 0;
+        if (f.kc && lane < width / 16) {
+            *(uint4*)(f.kc + at + 16 * lane) = *(uint4*)(f.kc + second + at + 16 * lane) = uint4{};
+            if (lane < width / 32) f.ks[at / 32 + lane] = f.ks[(second + at) / 32 + lane] = 0;
+        }
+    }
+}
+template <typename T>
+__device__ __forceinline__ void zero_backward(const MxFfnArgs& f, int64_t m0, int rows, int64_t n0, int cols, int t) {
+    for (int r = __builtin_amdgcn_readfirstlane(t >> 6); r < rows; r += 4)
+        for (int k = t & 63; k < cols; k += 64) {
+            T* const p = (T*)f.g.c + (m0 + r) * f.g.ldc + n0 + k;
+            store_c(p, 0.0f);
+            store_c(p + f.g.N, 0.0f);
+            if (f.h) store_c((T*)f.h + (m0 + r) * f.ldh + n0 + k, 0.0f);
+        }
 }
 
 // ---------------------------------------------------------------- host
 inline int mx8_check_tensor(const mxfp8_tensor* t, bool used) {
     return mx_check_tensor((const mxfp4_tensor*)t, used);
 }
+// The tiled kernels (mx_ffn_forward256.hip and so on); mode: MxDense or MxRows.
+int mx_forward256(const MxFfnArgs& f, int mode, int dtype, int act, hipStream_t st);
+int mx_backward256(const MxFfnArgs& f, int mode, int dtype, int act, hipStream_t st);
+int mx_forward128(const MxFfnArgs& f, int mode, int dtype, int act, hipStream_t st);
+int mx_backward128(const MxFfnArgs& f, int mode, int dtype, int act, hipStream_t st);
 inline bool mx_activation(int32_t a) { return a == MXFP4_SILU || a == MXFP4_GELU; }
 
 }  // namespace nvfp4

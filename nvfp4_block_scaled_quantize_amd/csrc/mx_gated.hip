@@ -1,79 +1,27 @@
-// mx_gated.hip -- the gated feed-forward block on MXFP4 products: the entry points, and a plain kernel.
+// mx_gated.hip -- the gated feed-forward block on MXFP4 products: the entry points.
 //
 // Forward: G and U are the products of A with the two halves of W, H = a(G) U.  Backward: dH is a
 // product, dG and dU follow from it and the checkpoint's G and U.  Either way what is done to an
 // element needs no other but those of its block of 32, which a lane pair holds, so it is done to the
 // accumulators and nothing but the results goes to memory.
-//
-// The plain kernel: a wave computes 32 x 32 of H, or of dH, with its operands straight from memory.
 #include "mx_ffn.h"
 
 namespace nvfp4 {
 
-// A fragment's 16 bytes for a lane: row `row` of an operand, K step s (of 64 elements).
-__device__ __forceinline__ int4v plain_codes(const uint8_t* p, int64_t row, int64_t pitch, int64_t s, int h) {
-    return *(const int4v*)(p + row * pitch + s * 32 + h * 16);
-}
-
-template <typename T, int ACT, bool BACK, bool GROUPS>
-__global__ __launch_bounds__(256) void k_mx_gated(MxFfnArgs f, unsigned tiles_n, int64_t width) {
+// Which tile: the rule of the plain products (mx_gemm.hip), by the rows of B.
+template <int KIND>
+static int launch_tiles(const MxFfnArgs& f, int dtype, int act, hipStream_t st) {
     const MxGArgs& g = f.g;
-    const int lane = threadIdx.x & 63, wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int li = lane & 31, h = lane >> 5;
-    const int64_t pitch = g.kp / 2, spitch = g.kp / 32;
-    unsigned tm, tn;
-    int64_t m0, rows;
-    const uint8_t *bc = g.bc, *bs = g.bs;
-    int64_t steps = g.kp / 64;
-    bool none = false;
-    if constexpr (GROUPS) {
-        MxUnit u;
-        if (!mx_find_tile(g.offsets, g.n_groups, (int)g.M, 32, blockIdx.x, tiles_n, tm, tn, u)) return;
-        m0 = u.row0, rows = u.rows, none = u.group == g.n_groups;
-        if (none) steps = 0;
-        else bc += u.group * (BACK ? 1 : 2) * g.N * pitch, bs += u.group * (BACK ? 1 : 2) * g.N * spitch;
-    } else {
-        mx_tile_of(blockIdx.x, (unsigned)((g.M + 31) / 32), tiles_n, tm, tn);
-        m0 = (int64_t)tm * 32, rows = g.M - m0 < 32 ? g.M - m0 : 32;
-    }
-    const int64_t c0 = ((int64_t)tn * 4 + wid) * 32;
-    if (c0 >= width) return;
-    // rows and columns past the end repeat the last: their results are not stored
-    const int64_t ra = m0 + (li < rows ? li : rows - 1), rb = c0 + li < g.N ? c0 + li : g.N - 1;
-    float16v acc[BACK ? 1 : 2] = {};
-    for (int64_t s = 0; s < steps; ++s) {
-        const int4v a = plain_codes(g.ac, ra, pitch, s, h);
-        const int sa = g.as[ra * spitch + s * 2 + h];
-#pragma unroll
-        for (int j = 0; j < (BACK ? 1 : 2); ++j) {
-            const int64_t r = rb + j * g.N;
-            acc[j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(mx_frag(plain_codes(bc, r, pitch, s, h)), mx_frag(a), acc[j],
-                                                                     kE2M1, kE2M1, 0, bs[r * spitch + s * 2 + h], 0, sa);
-        }
-    }
-    const bool in = li < rows;
-    const int left = (int)(g.N - c0 < 32 ? g.N - c0 : 32);
-    if constexpr (BACK) put_backward<T, ACT>(f, acc[0], m0 + li, in, c0, left, h, none);
-    else put_forward<T, ACT>(f, acc[0], acc[1], m0 + li, in, c0, left, h);
-}
-
-template <typename T, int ACT, bool BACK>
-static int launch_plain(const MxFfnArgs& f, hipStream_t st) {
-    const MxGArgs& g = f.g;
-    const int64_t width = f.qc || f.kc ? f.np : g.N, tn = (width + 127) / 128;
-    // every group, and the rows in none, may end in a partial unit
-    const int64_t units = g.offsets ? g.M / 32 + (g.n_groups < g.M ? g.n_groups : g.M) + 1 : (g.M + 31) / 32;
-    if (!mx_grid_fits((__int128)units * tn, 256)) return NVFP4_ERR_SHAPE;
-    const auto kernel = g.offsets ? k_mx_gated<T, ACT, BACK, true> : k_mx_gated<T, ACT, BACK, false>;
-    kernel<<<dim3((unsigned)(units * tn)), 256, 0, st>>>(f, (unsigned)tn, width);
-    return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
-}
-
-template <bool BACK>
-static int launch_any(const MxFfnArgs& f, int dtype, int act, hipStream_t st) {
-    if (act == MXFP4_SILU)
-        return dtype == NVFP4_BF16 ? launch_plain<uint16_t, MXFP4_SILU, BACK>(f, st) : launch_plain<float, MXFP4_SILU, BACK>(f, st);
-    return dtype == NVFP4_BF16 ? launch_plain<uint16_t, MXFP4_GELU, BACK>(f, st) : launch_plain<float, MXFP4_GELU, BACK>(f, st);
+    const int mode = g.n_groups ? MxRows : MxDense;
+    const auto tiles = [&](int64_t side) {
+        int64_t m = (g.M + side - 1) / side;
+        if (mode == MxRows) m = (2 * g.M / side + (g.n_groups < g.M ? g.n_groups : g.M) + 1) / 2;
+        return m * ((kMxWeights<KIND> * g.N + side - 1) / side);
+    };
+    const int64_t big = (tiles(256) + 255) / 256 * 100, n = tiles(128), rest = n % 512;
+    const int64_t small = n / 512 * 68 + (rest == 0 ? 0 : rest <= 256 ? 45 : 68);
+    if constexpr (KIND == kForward) return big <= small ? mx_forward256(f, mode, dtype, act, st) : mx_forward128(f, mode, dtype, act, st);
+    else return big <= small ? mx_backward256(f, mode, dtype, act, st) : mx_backward128(f, mode, dtype, act, st);
 }
 
 // Extents as in mxfp4_gemm, for a product of 2 N columns.
@@ -119,7 +67,7 @@ extern "C" int mxfp4_gated(const mxfp4_tensor* a, const mxfp4_tensor* w, const i
                    mx_above(scale_rule), nullptr, nullptr, nullptr, nullptr, mx_pad(N), nullptr, 0};
     if (h_copy) f.qc = h_copy->codes, f.qs = h_copy->scales;
     if (checkpoint) f.kc = checkpoint->codes, f.ks = checkpoint->scales;
-    return launch_any<false>(f, h ? h_dtype : NVFP4_F32, activation, (hipStream_t)stream);
+    return launch_tiles<kForward>(f, h ? h_dtype : NVFP4_F32, activation, (hipStream_t)stream);
 }
 
 static size_t linear_code_bytes(int64_t M, int64_t K) {
@@ -168,5 +116,5 @@ extern "C" int mxfp4_gated_backward(const mxfp4_tensor* dy, const mxfp4_tensor* 
     if (!used) return NVFP4_OK;
     const MxFfnArgs f = {{dy->codes, dy->scales, w->codes, w->scales, M, N, mx_pad(K), 0, dgu, ld, offsets, (int)n_groups},
                          0, nullptr, nullptr, checkpoint->codes, checkpoint->scales, mx_pad(N), h, ldh};
-    return launch_any<true>(f, dtype, activation, (hipStream_t)stream);
+    return launch_tiles<kBackward>(f, dtype, activation, (hipStream_t)stream);
 }

@@ -140,3 +140,10 @@ def test_library_that_lacks_them(kind, tmp_path, monkeypatch):
             with pytest.raises(nv.Nvfp4Error, match="rebuild"):
                 nv.mxfp4_gated_linear_workspace_bytes(1, 32, 32)
     assert nv.mxfp4_linear_workspace_bytes(1, 32, 32) == 0 and nv.load_library().nvfp4_abi_version() == nv.ABI_VERSION
+
+
+@pytest.mark.parametrize("source", ["mx_ffn_forward128.hip", "mx_ffn_forward256.hip", "mx_ffn_backward128.hip", "mx_ffn_backward256.hip"])
+def test_nothing_else_writes_m0(source):
+    """As of the plain products' kernels: several direct loads share what one instruction set M0 to."""
+    import test_direct_load_m0_cpu
+    test_direct_load_m0_cpu.test_nothing_else_writes_m0(source)
