@@ -40,11 +40,11 @@ __global__ __launch_bounds__(256) void k_mx8_quantize(Mx8Args g) {
     for (int i = 0; i < kSteps8; ++i) {
         const int64_t at = first + threadIdx.x + 256 * i;   // oct of the checkpoint
         const uint32_t code = mx8_scale_code(quad_max(max_bits(o[i])));
-        const float inv = mx8_inverse(code);
+        const float scale = mx_scale_value(code);
         uint32_t w[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            w[j] = mx8_codes(value(o[i], 4 * j), value(o[i], 4 * j + 1), value(o[i], 4 * j + 2), value(o[i], 4 * j + 3), inv);
+            w[j] = mx8_codes(value(o[i], 4 * j), value(o[i], 4 * j + 1), value(o[i], 4 * j + 2), value(o[i], 4 * j + 3), scale);
             if (code == 255u) w[j] = 0;
         }
         if (at < total) {

@@ -17,12 +17,14 @@ __device__ __forceinline__ uint32_t mx8_scale_code(uint32_t amax_bits) {
     return (e > 8u ? e : 8u) - 8u;
 }
 
-// Four codes.  inv: 1 / scale, a power of two from mx8_inverse; the products are exact but for
-// those below 2^-126, whose code is a zero either way, and none exceeds 448.
-__device__ __forceinline__ float mx8_inverse(uint32_t code) { return __uint_as_float((254u - code) << 23); }
-__device__ __forceinline__ uint32_t mx8_codes(float a, float b, float c, float d, float inv) {
-    const int w = __builtin_amdgcn_cvt_pk_fp8_f32(a * inv, b * inv, 0, false);
-    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c * inv, d * inv, w, true);
+// Four codes.  The conversion takes the scale, mx_scale_value(code), as an operand and divides by it
+// exactly; nothing exceeds 448.
+typedef short short2v __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t mx8_codes(float a, float b, float c, float d, float scale) {
+    short2v w = {0, 0};
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, a, b, scale, false);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, c, d, scale, true);
+    return __builtin_bit_cast(uint32_t, w);
 }
 
 // The scale of a code as a factor; NaN for 255.
@@ -36,6 +38,13 @@ struct Quad {
 __device__ __forceinline__ Quad mx8_values(uint32_t w, float s) {
     const float2v a = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false), b = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, true);
     return {{a[0] * s, a[1] * s, b[0] * s, b[1] * s}};
+}
+
+// The same by the conversion's own scale operand, for scale codes up to 254.
+__device__ __forceinline__ Quad mx8_scaled(uint32_t w, uint32_t code) {
+    const float s = mx_scale_value(code);
+    const float2v a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w, s, false), b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w, s, true);
+    return {{a[0], a[1], b[0], b[1]}};
 }
 
 // ---------------------------------------------------------------- activations
@@ -52,15 +61,15 @@ template <int ACT>
 __device__ __forceinline__ float act_value(float x) {
     return x * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(act_arg<ACT>(x)));
 }
-// a(x) and a'(x) = S + x S (1 - S) y', y' = 1 or 2 z'.  1 - S as it stands where S is small (2^-y may
-// be infinite there), as 2^-y S where the difference would cancel.
+// a(x) and a'(x) = S + x S (1 - S) y', y' = 1 or 2 z'.  The difference 1 - S is off by half a step of 1 or
+// less, which against a' near 1 is |x y'| such steps.
 struct Act {
     float a, slope;
 };
 template <int ACT>
 __device__ __forceinline__ Act act_both(float x) {
-    const float e = __builtin_amdgcn_exp2f(act_arg<ACT>(x)), s = __builtin_amdgcn_rcpf(1.0f + e);
-    const float t = s < 0.5f ? 1.0f - s : e * s, a = x * s;
+    const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(act_arg<ACT>(x)));
+    const float t = 1.0f - s, a = x * s;
     if constexpr (ACT == MXFP4_SILU) return {a, __builtin_fmaf(a, t, s)};
     else return {a, __builtin_fmaf(a * t, __builtin_fmaf(6.0f * kGeluB, x * x, 2.0f * kGeluA), s)};
 }
@@ -84,12 +93,16 @@ __device__ __forceinline__ void swap_halves(uint32_t& a, uint32_t& b) {
     a = r[0], b = r[1];
 }
 
-// The largest magnitude (its bits) of a row's 32 elements: 16 in this lane, 16 in lane ^ 32.
+// The largest magnitude (its bits) of a row's 32 elements: 16 in this lane, 16 in lane ^ 32.  As signed
+// numbers the bits of the positive ones order as their values do, as unsigned ones those of the negative ones
+// do and lie above the others.
 __device__ __forceinline__ uint32_t block_max(const float16v& x) {
-    uint32_t m = 0;
+    int p = __float_as_int(x[0]);
+    uint32_t n = __float_as_uint(x[0]);
 #pragma unroll
-    for (int r = 0; r < 16; ++r) m = max(m, __float_as_uint(x[r]) & 0x7FFFFFFFu);
-    uint32_t o = m;
+    for (int r = 1; r < 16; ++r) p = max(p, __float_as_int(x[r])), n = max(n, __float_as_uint(x[r]));
+    // (without a negative one n is p; without a positive one p has the sign set)
+    uint32_t m = max((uint32_t)max(p, 0), n & 0x7FFFFFFFu), o = m;
     swap_halves(m, o);
     return max(m, o);
 }
@@ -97,45 +110,109 @@ __device__ __forceinline__ uint32_t block_max(const float16v& x) {
 // A 32 x 32 block as the matrix instructions leave it: lane l holds row l mod 32, and in register r
 // column 8 (r / 4) + 4 (l / 32) + r mod 4.
 //
-// Its MXFP4 copy: codes at `codes` (16 bytes of the row), the scale at `scale`.  A lane makes a half of
-// each of the row's four dwords; the halves of the wave exchange them so that each lane has two.
-__device__ __forceinline__ void put_copy_block(const float16v& x, uint32_t above, uint8_t* codes, uint8_t* scale,
-                                               int h, bool in) {
-    const uint32_t code = mx_scale_code(block_max(x), above);
+// Its E2M1 codes, and the scale's: w[i] holds the lane's halves of dwords 2 i and 2 i + 1 of the row's four.
+// `past`: no column of it exists.  (Those of a block that some of exist in are zeros, or of a row that is NaN.)
+__device__ __forceinline__ uint32_t copy_codes(const float16v& x, uint32_t above, bool past, uint32_t (&w)[2]) {
+    const uint32_t code = past ? 0u : mx_scale_code(block_max(x), above);
     const float cs = mx_scale_value(code);
-    uint32_t w[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         w[i] = cvt_fp4x2<0>(0u, x[8 * i], x[8 * i + 1], cs);
         w[i] = cvt_fp4x2<1>(w[i], x[8 * i + 2], x[8 * i + 3], cs);
         w[i] = cvt_fp4x2<2>(w[i], x[8 * i + 4], x[8 * i + 5], cs);
         w[i] = cvt_fp4x2<3>(w[i], x[8 * i + 6], x[8 * i + 7], cs);
-        if (code == 255u) w[i] = 0;
+        if (code == 255u || past) w[i] = 0;
     }
-    swap_halves(w[0], w[1]);
-    if (!in) return;
-    *(uint2*)(codes + 8 * h) = make_uint2(__builtin_amdgcn_perm(w[1], w[0], 0x05040100u),
-                                          __builtin_amdgcn_perm(w[1], w[0], 0x07060302u));
-    if (h == 0) *scale = (uint8_t)code;
+    return code;
+}
+// Two dwords from this lane's halves (`a` of the wave's lower lanes, `b` of its upper ones) of both.
+__device__ __forceinline__ void join_halves(uint32_t a, uint32_t b, uint32_t& first, uint32_t& second) {
+    first = __builtin_amdgcn_perm(b, a, 0x05040100u), second = __builtin_amdgcn_perm(b, a, 0x07060302u);
+}
+// The MXFP4 copy of J blocks side by side: 16 J bytes of codes of the row at `codes`, the scales at `scale`.  The
+// wave's halves exchange what they hold of each other's dwords: of one block each has two then, of two blocks all
+// four of one of them.
+template <int J>
+__device__ __forceinline__ void put_copy(const float16v (&x)[J], uint32_t above, uint8_t* codes, uint8_t* scale, int left, int h,
+                                         bool in) {
+    static_assert(J == 1 || J == 2);
+    uint32_t w[2][2], code[2], d[4];
+#pragma unroll
+    for (int j = 0; j < J; ++j) code[j] = copy_codes(x[j], above, left <= 32 * j, w[j]);
+    if constexpr (J == 1) {
+        swap_halves(w[0][0], w[0][1]);
+        join_halves(w[0][0], w[0][1], d[0], d[1]);
+        if (!in) return;
+        *(uint2*)(codes + 8 * h) = make_uint2(d[0], d[1]);
+        if (h == 0) *scale = (uint8_t)code[0];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            swap_halves(w[0][i], w[1][i]);
+            join_halves(w[0][i], w[1][i], d[2 * i], d[2 * i + 1]);
+        }
+        if (!in) return;
+        *(uint4*)(codes + 16 * h) = make_uint4(d[0], d[1], d[2], d[3]);
+        if (h == 0) *(uint16_t*)scale = (uint16_t)(code[0] | code[1] << 8);
+    }
 }
 
-// Its checkpoint: 32 bytes of the row at `codes`, 16 of them a lane's.
-__device__ __forceinline__ void put_checkpoint_block(const float16v& x, uint8_t* codes, uint8_t* scale, int h, bool in) {
-    const uint32_t code = mx8_scale_code(block_max(x));
-    const float inv = mx8_inverse(code);
-    uint32_t d[4];
+// A block's E4M3 codes, and the scale's: d[q] of columns 8 q + 4 h .. + 3.
+__device__ __forceinline__ uint32_t checkpoint_codes(const float16v& x, bool past, uint32_t (&d)[4]) {
+    const uint32_t code = past ? 0u : mx8_scale_code(block_max(x));
+    const float scale = mx_scale_value(code);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-        d[q] = mx8_codes(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3], inv);
-        if (code == 255u) d[q] = 0;
+        d[q] = mx8_codes(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3], scale);
+        if (code == 255u || past) d[q] = 0;
     }
-    swap_halves(d[0], d[2]);
-    swap_halves(d[1], d[3]);
-    if (!in) return;
-    *(uint4*)(codes + 16 * h) = make_uint4(d[0], d[2], d[1], d[3]);
-    if (h == 0) *scale = (uint8_t)code;
+    return code;
 }
-// And back: the lane's 16 bytes, as they lie there, to the dwords of its four columns each.
+// The checkpoint of 32 rows: J blocks side by side of G, and of U `second` elements on; `at`: of row 0.  A
+// block's 32 bytes of a row are exchanged between the wave's halves, two blocks' 64 go through LDS.  The lower half
+// of the wave stores the scales of G, the upper one those of U.
+template <int J>
+__device__ __forceinline__ void put_checkpoint(const float16v (&g)[J], const float16v (&u)[J], uint8_t* piece, uint8_t* kc,
+                                               uint8_t* ks, int64_t at, int64_t np, int64_t second, int rows, int left, int lane) {
+    static_assert(J == 1 || J == 2);
+    const int h = lane >> 5, li = lane & 31;
+    uint32_t gs = 0, us = 0;
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            uint32_t d[4];
+            const uint32_t code = checkpoint_codes(t ? u[j] : g[j], left <= 32 * j, d);
+            (t ? us : gs) |= code << (8 * j);
+            if constexpr (J == 1) {
+                swap_halves(d[0], d[2]);
+                swap_halves(d[1], d[3]);
+                if (li < rows) *(uint4*)(kc + t * second + at + li * np + 16 * h) = make_uint4(d[0], d[2], d[1], d[3]);
+            } else {
+                // 64 bytes a row; its chunks of 16 in an order that changes every four rows, which the banks repeat in
+                uint8_t* p = piece + t * 2048 + li * 64 + 4 * h;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) *(uint32_t*)(p + (((2 * j + q / 2) ^ ((li >> 2) & 3)) << 4) + 8 * (q & 1)) = d[q];
+            }
+        }
+    if constexpr (J == 2) {
+        const int row = lane >> 2, c = lane & 3;
+        const uint8_t* p = piece + row * 64 + ((c ^ ((row >> 2) & 3)) << 4);
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const uint4 v = *(const uint4*)(p + t * 2048 + k * 1024);
+                if (row + 16 * k < rows) *(uint4*)(kc + t * second + at + (row + 16 * k) * np + 16 * c) = v;
+            }
+    }
+    if (li < rows) {
+        const int64_t s = ((h ? second : 0) + at + li * np) / 32;
+        if constexpr (J == 1) ks[s] = (uint8_t)(h ? us : gs);
+        else *(uint16_t*)(ks + s) = (uint16_t)(h ? us : gs);
+    }
+}
+// And back: the lane's 16 bytes of a block, as they lie in the row, to the dwords of its four columns each.
 __device__ __forceinline__ void spread_checkpoint(uint4 v, uint32_t (&d)[4]) {
     d[0] = v.x, d[2] = v.y, d[1] = v.z, d[3] = v.w;
     swap_halves(d[0], d[2]);
@@ -198,97 +275,84 @@ __device__ __forceinline__ void put_rows(uint8_t* piece, const float16v (&x)[J],
 }
 
 // The forward's results from J blocks of G and as many of U: rows from m0, of which `rows` exist, columns from
-// c0, of which `left` are below N (the rest are zeros in the copies, whose rows reach to np).
+// c0, of which `left` are below N: the rest are zeros, products of B's rows past the end, which the copies'
+// rows, up to np, hold.
 template <typename T, int ACT, int J>
-__device__ __forceinline__ void forward_rows(const MxFfnArgs& f, float16v (&g)[J], float16v (&u)[J], uint8_t* piece, int64_t m0,
+__device__ __forceinline__ void forward_rows(const MxFfnArgs& f, const float16v (&g)[J], const float16v (&u)[J], uint8_t* piece, int64_t m0,
                                              int rows, int64_t c0, int left, bool whole, int lane) {
     const int h = lane >> 5, li = lane & 31;
     float16v x[J];
 #pragma unroll
     for (int j = 0; j < J; ++j)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            if (!whole && 32 * j + 8 * (r / 4) + 4 * h + r % 4 >= left) g[j][r] = u[j][r] = 0.0f;
-            x[j][r] = act_value<ACT>(g[j][r]) * u[j][r];
-        }
+        for (int r = 0; r < 16; ++r) x[j][r] = act_value<ACT>(g[j][r]) * u[j][r];
     if (f.g.c) put_rows<T, J>(piece, x, (T*)f.g.c + m0 * f.g.ldc + c0, f.g.ldc, rows, left, whole, lane);
     if (!f.qc && !f.kc) return;
-    const int64_t at = (m0 + li) * f.np + c0, second = f.g.M * f.np;
-    const bool in = li < rows && c0 < f.np;
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-        const int64_t b = at + 32 * j;
-        if (f.qc) put_copy_block(x[j], f.above, f.qc + b / 2, f.qs + b / 32, h, in);
-        if (f.kc) {
-            put_checkpoint_block(g[j], f.kc + b, f.ks + b / 32, h, in);
-            put_checkpoint_block(u[j], f.kc + second + b, f.ks + (second + b) / 32, h, in);
-        }
-    }
+    const int have = c0 < f.np ? rows : 0;
+    const int64_t at = m0 * f.np + c0, b = at + li * f.np;
+    if (f.qc) put_copy<J>(x, f.above, f.qc + b / 2, f.qs + b / 32, left, h, li < have);
+    if (f.kc) put_checkpoint<J>(g, u, piece, f.kc, f.ks, at, f.np, f.g.M * f.np, have, left, lane);
 }
 // The stores at least that a wave issues for `groups` times 32 whole rows of J blocks: 128 bytes x 8 rows of a
-// tensor each, one a block of the copy's codes, and two of the checkpoint's.
+// tensor each, one a pair of blocks of the copy's codes, and two a block of the checkpoint's.
 template <typename T>
 __device__ __forceinline__ int forward_stores(const MxFfnArgs& f, int groups, int blocks) {
-    return groups * blocks * ((f.g.c ? (int)sizeof(T) : 0) + (f.qc ? 1 : 0) + (f.kc ? 2 : 0));
+    return groups * (blocks * ((f.g.c ? (int)sizeof(T) : 0) + (f.kc ? 2 : 0)) + (f.qc ? 1 : 0));
 }
 
-// J blocks of the checkpoint in a row: its 16 J code bytes of G and of U that this lane decodes, and the scales.
-template <int J>
+// Two blocks of the checkpoint in a row: the 32 code bytes of G and of U that this lane decodes, and the scales.
 struct Kept {
-    uint4 g[J], u[J];
+    uint4 g[2], u[2];
     uint32_t gs, us;
 };
-// Of row m (or the last there is), columns from c0, a multiple of 32 J.  No branch but one that is the same
-// for the whole wave: a join would wait for the loads.
-template <int J>
-__device__ __forceinline__ Kept<J> load_kept(const MxFfnArgs& f, int64_t m, int64_t c0, int h) {
-    using Scales = std::conditional_t<J == 4, uint32_t, uint16_t>;
-    static_assert(J == 4 || J == 2);
+// Of row m (or the last there is), columns from c0, a multiple of 64.  No branch: a join would wait for the loads.
+__device__ __forceinline__ Kept load_kept(const MxFfnArgs& f, int64_t m, int64_t c0, int h) {
     c0 = c0 < f.np ? c0 : 0;        // (nothing of it will be stored)
     const int64_t at = (m < f.g.M ? m : f.g.M - 1) * f.np + c0, second = f.g.M * f.np;
-    Kept<J> k;
+    Kept k;
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
+    for (int j = 0; j < 2; ++j) {
         k.g[j] = *(const uint4*)(f.kc + at + 32 * j + 16 * h);
         k.u[j] = *(const uint4*)(f.kc + second + at + 32 * j + 16 * h);
     }
-    k.gs = *(const Scales*)(f.ks + at / 32);
-    k.us = *(const Scales*)(f.ks + (second + at) / 32);
+    k.gs = *(const uint16_t*)(f.ks + at / 32);
+    k.us = *(const uint16_t*)(f.ks + (second + at) / 32);
     return k;
 }
 
-// The backward's results from J blocks d of dH and the checkpoint's.
-template <typename T, int ACT, int J>
-__device__ __forceinline__ void backward_rows(const MxFfnArgs& f, const float16v (&d)[J], const Kept<J>& kept, uint8_t* piece,
+// The backward's results from two blocks d of dH and the checkpoint's.
+template <typename T, int ACT>
+__device__ __forceinline__ void backward_rows(const MxFfnArgs& f, const float16v (&d)[2], const Kept& kept, uint8_t* piece,
                                               int64_t m0, int rows, int64_t c0, int left, bool whole, int lane) {
-    T* const pg = (T*)f.g.c + m0 * f.g.ldc + c0;
-    T* const ph = (T*)f.h + m0 * f.ldh + c0;
+    float16v dg[2], du[2], x[2];
 #pragma unroll
-    for (int p = 0; p < J; p += 2) {
-        float16v dg[2], du[2], x[2];
+    for (int j = 0; j < 2; ++j) {
+        uint32_t gw[4], uw[4];
+        spread_checkpoint(kept.g[j], gw);
+        spread_checkpoint(kept.u[j], uw);
+        const uint32_t gs = (kept.gs >> (8 * j)) & 0xFFu, us = (kept.us >> (8 * j)) & 0xFFu;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            uint32_t gw[4], uw[4];
-            spread_checkpoint(kept.g[p + j], gw);
-            spread_checkpoint(kept.u[p + j], uw);
-            const float gs = mx8_factor((kept.gs >> (8 * (p + j))) & 0xFFu), us = mx8_factor((kept.us >> (8 * (p + j))) & 0xFFu);
+        for (int q = 0; q < 4; ++q) {
+            const Quad g = mx8_scaled(gw[q], gs), u = mx8_scaled(uw[q], us);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const Quad g = mx8_values(gw[q], gs), u = mx8_values(uw[q], us);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const Act a = act_both<ACT>(g.v[i]);
-                    const float v = d[p + j][4 * q + i];
-                    du[j][4 * q + i] = v * a.a;
-                    dg[j][4 * q + i] = v * u.v[i] * a.slope;
-                    x[j][4 * q + i] = a.a * u.v[i];
-                }
+            for (int i = 0; i < 4; ++i) {
+                const Act a = act_both<ACT>(g.v[i]);
+                const float v = d[j][4 * q + i];
+                du[j][4 * q + i] = v * a.a;
+                dg[j][4 * q + i] = v * u.v[i] * a.slope;
+                x[j][4 * q + i] = a.a * u.v[i];
             }
         }
-        put_rows<T, 2>(piece, dg, pg + 32 * p, f.g.ldc, rows, left - 32 * p, whole, lane);
-        put_rows<T, 2>(piece, du, pg + f.g.N + 32 * p, f.g.ldc, rows, left - 32 * p, whole, lane);
-        if (f.h) put_rows<T, 2>(piece, x, ph + 32 * p, f.ldh, rows, left - 32 * p, whole, lane);
+        if (__builtin_amdgcn_ballot_w64(gs == 255u || us == 255u)) {     // blocks of NaN are rare
+            const float both = gs == 255u || us == 255u ? __builtin_nanf("") : 0.0f, gate = gs == 255u ? __builtin_nanf("") : 0.0f;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) dg[j][r] += both, x[j][r] += both, du[j][r] += gate;
+        }
     }
+    T* const p = (T*)f.g.c + m0 * f.g.ldc + c0;
+    put_rows<T, 2>(piece, dg, p, f.g.ldc, rows, left, whole, lane);
+    put_rows<T, 2>(piece, du, p + f.g.N, f.g.ldc, rows, left, whole, lane);
+    if (f.h) put_rows<T, 2>(piece, x, (T*)f.h + m0 * f.ldh + c0, f.ldh, rows, left, whole, lane);
 }
 
 // The results of `rows` rows in no group, `width` columns from n0, by a workgroup of 256.
@@ -323,9 +387,8 @@ __device__ __forceinline__ void zero_backward(const MxFfnArgs& f, int64_t m0, in
 inline int mx8_check_tensor(const mxfp8_tensor* t, bool used) {
     return mx_check_tensor((const mxfp4_tensor*)t, used);
 }
-// The tiled kernels (mx_ffn_forward256.hip and so on); mode: MxDense or MxRows.
-int mx_forward256(const MxFfnArgs& f, int mode, int dtype, int act, hipStream_t st);
-int mx_backward256(const MxFfnArgs& f, int mode, int dtype, int act, hipStream_t st);
+// The tiled kernels (mx_ffn_forward256.hip and so on; that one for bfloat16 alone); mode: MxDense or MxRows.
+int mx_forward256(const MxFfnArgs& f, int mode, int act, hipStream_t st);
 int mx_forward128(const MxFfnArgs& f, int mode, int dtype, int act, hipStream_t st);
 int mx_backward128(const MxFfnArgs& f, int mode, int dtype, int act, hipStream_t st);
 inline bool mx_activation(int32_t a) { return a == MXFP4_SILU || a == MXFP4_GELU; }

@@ -3,16 +3,14 @@
 
 namespace nvfp4 {
 
-template <typename T, int ACT>
+template <int ACT>
 static int launch_mode(const MxFfnArgs& f, int mode, hipStream_t st) {
-    return mode == MxDense ? tile256::launch<T, MxDense, sizeof(T) == 2, kForward, ACT>(f, st)
-                           : tile256::launch<T, MxRows, sizeof(T) == 2, kForward, ACT>(f, st);
+    return mode == MxDense ? tile256::launch<uint16_t, MxDense, true, kForward, ACT>(f, st)
+                           : tile256::launch<uint16_t, MxRows, true, kForward, ACT>(f, st);
 }
 
-int mx_forward256(const MxFfnArgs& f, int mode, int dtype, int act, hipStream_t st) {
-    if (act == MXFP4_SILU)
-        return dtype == NVFP4_BF16 ? launch_mode<uint16_t, MXFP4_SILU>(f, mode, st) : launch_mode<float, MXFP4_SILU>(f, mode, st);
-    return dtype == NVFP4_BF16 ? launch_mode<uint16_t, MXFP4_GELU>(f, mode, st) : launch_mode<float, MXFP4_GELU>(f, mode, st);
+int mx_forward256(const MxFfnArgs& f, int mode, int act, hipStream_t st) {
+    return act == MXFP4_SILU ? launch_mode<MXFP4_SILU>(f, mode, st) : launch_mode<MXFP4_GELU>(f, mode, st);
 }
 
 }  // namespace nvfp4

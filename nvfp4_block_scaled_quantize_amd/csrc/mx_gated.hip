@@ -8,20 +8,20 @@
 
 namespace nvfp4 {
 
-// Which tile: the rule of the plain products (mx_gemm.hip), by the rows of B.
-template <int KIND>
-static int launch_tiles(const MxFfnArgs& f, int dtype, int act, hipStream_t st) {
+// Which tile of the forward, in percent of a round of 256 large ones (as in mx_gemm.hip): 512 small ones take 55,
+// up to 256 of them 37, and where rows are grouped a large tile's ends cost more.  (RULE)
+static int launch_forward(const MxFfnArgs& f, int dtype, int act, hipStream_t st) {
     const MxGArgs& g = f.g;
     const int mode = g.n_groups ? MxRows : MxDense;
     const auto tiles = [&](int64_t side) {
         int64_t m = (g.M + side - 1) / side;
         if (mode == MxRows) m = (2 * g.M / side + (g.n_groups < g.M ? g.n_groups : g.M) + 1) / 2;
-        return m * ((kMxWeights<KIND> * g.N + side - 1) / side);
+        return m * ((2 * g.N + side - 1) / side);
     };
-    const int64_t big = (tiles(256) + 255) / 256 * 100, n = tiles(128), rest = n % 512;
-    const int64_t small = n / 512 * 68 + (rest == 0 ? 0 : rest <= 256 ? 45 : 68);
-    if constexpr (KIND == kForward) return big <= small ? mx_forward256(f, mode, dtype, act, st) : mx_forward128(f, mode, dtype, act, st);
-    else return big <= small ? mx_backward256(f, mode, dtype, act, st) : mx_backward128(f, mode, dtype, act, st);
+    const int64_t big = (tiles(256) + 255) / 256 * (mode == MxRows ? 125 : 100), n = tiles(128), rest = n % 512;
+    const int64_t small = n / 512 * 55 + (rest == 0 ? 0 : rest <= 256 ? 37 : 55);
+    if (dtype == NVFP4_BF16 && big <= small) return mx_forward256(f, mode, act, st);
+    return mx_forward128(f, mode, dtype, act, st);
 }
 
 // Extents as in mxfp4_gemm, for a product of 2 N columns.
@@ -67,7 +67,7 @@ extern "C" int mxfp4_gated(const mxfp4_tensor* a, const mxfp4_tensor* w, const i
                    mx_above(scale_rule), nullptr, nullptr, nullptr, nullptr, mx_pad(N), nullptr, 0};
     if (h_copy) f.qc = h_copy->codes, f.qs = h_copy->scales;
     if (checkpoint) f.kc = checkpoint->codes, f.ks = checkpoint->scales;
-    return launch_tiles<kForward>(f, h ? h_dtype : NVFP4_F32, activation, (hipStream_t)stream);
+    return launch_forward(f, h ? h_dtype : NVFP4_BF16, activation, (hipStream_t)stream);
 }
 
 static size_t linear_code_bytes(int64_t M, int64_t K) {
@@ -116,5 +116,5 @@ extern "C" int mxfp4_gated_backward(const mxfp4_tensor* dy, const mxfp4_tensor* 
     if (!used) return NVFP4_OK;
     const MxFfnArgs f = {{dy->codes, dy->scales, w->codes, w->scales, M, N, mx_pad(K), 0, dgu, ld, offsets, (int)n_groups},
                          0, nullptr, nullptr, checkpoint->codes, checkpoint->scales, mx_pad(N), h, ldh};
-    return launch_tiles<kBackward>(f, dtype, activation, (hipStream_t)stream);
+    return mx_backward128(f, n_groups ? MxRows : MxDense, dtype, activation, (hipStream_t)stream);
 }

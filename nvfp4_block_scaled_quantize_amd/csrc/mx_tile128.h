@@ -85,6 +85,10 @@ __global__ __launch_bounds__(256, SLOTS == 2 ? 2 : 1) void k_mx_tile128(MxKindAr
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
 
+    // The checkpoint's part of a wave's first 32 rows is asked for here, that of the others after the product.
+    [[maybe_unused]] Kept kept;
+    if constexpr (KIND == kBackward) kept = load_kept(args, m0 + wm * 64 + li, n0 + wn * 64, h);
+
     if (kbytes > 0) {
         const int nst = (kbytes + kRow - 1) / kRow;
         const int ra = (int)(m1 - m0 < kSide ? m1 - m0 : kSide), rb = (int)(g.N - n0 < kCols ? g.N - n0 : kCols);
@@ -241,16 +245,15 @@ __global__ __launch_bounds__(256, SLOTS == 2 ? 2 : 1) void k_mx_tile128(MxKindAr
         if constexpr (KIND == kForward) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                float16v gate[1] = {acc[i][0]}, up[1] = {acc[i][1]};
+                const float16v gate[1] = {acc[i][0]}, up[1] = {acc[i][1]};
                 forward_rows<T, ACT, 1>(args, gate, up, piece, r0 + i * 32, rows - i * 32, c0, left, whole, lane);
             }
         } else {
-            Kept<2> kept = load_kept<2>(args, r0 + li, c0, h);
+            const Kept next = load_kept(args, r0 + 32 + li, c0, h);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const Kept<2> now = kept;
-                if (i == 0) kept = load_kept<2>(args, r0 + 32 + li, c0, h);
-                backward_rows<T, ACT, 2>(args, acc[i], now, piece, r0 + i * 32, rows - i * 32, c0, left, whole, lane);
+                const Kept& now = i ? next : kept;
+                backward_rows<T, ACT>(args, acc[i], now, piece, r0 + i * 32, rows - i * 32, c0, left, whole, lane);
             }
         }
         return;

@@ -40,10 +40,10 @@
 // Matrix instructions alone, on all compute units with operands in registers, run at 6.5 PFLOP/s
 // (1.6 GHz) on random ones, at 9.3 on zeros.
 //
-// The gated feed-forward block (KIND) differs in what B's rows are and in what becomes of the accumulators.
-// Forward: a tile is 256 x 128 of H, its 256 rows of B 128 of the gate and 128 of the up projection, in LDS
-// such that wave (wm, wn) has the gate's columns 64 wn .. + 63 in accumulators 0 and 1 and the same of the
-// up projection in 2 and 3.  Backward: a tile of dH as above.
+// The gated feed-forward block's forward (KIND) differs in what B's rows are and in what becomes of the
+// accumulators: a tile is 256 x 128 of H, its 256 rows of B 128 of the gate and 128 of the up projection, in
+// LDS such that wave (wm, wn) has the gate's columns 64 wn .. + 63 in accumulators 0 and 1 and the same of the
+// up projection in 2 and 3.
 #pragma once
 #include "mx_tile.h"
 #include "mx_ffn.h"
@@ -57,11 +57,11 @@ constexpr int kScaleBuf = kTile * 32;                // one operand, four stages
 constexpr int kScalesAt = 2 * kSlot;                 // LDS offset of the scale buffers
 constexpr int kTileLds = kScalesAt + 4 * kScaleBuf;
 static_assert(kTileLds <= kMxMaxLds, "LDS budget");
-// Waits for all but the ten newest operations, or, of the ffn kinds, the 10 + `stores` if these are 8, 16 or 32.
+// Waits for all but the ten newest operations, or, of the forward kind, the 10 + 4, 16 or 32 if it issued as many `stores`.
 __device__ __forceinline__ void wait_10_and_barrier(int stores) {
     if (stores >= 32) asm volatile("s_waitcnt vmcnt(42)" ::: "memory");
     else if (stores >= 16) asm volatile("s_waitcnt vmcnt(26)" ::: "memory");
-    else if (stores >= 8) asm volatile("s_waitcnt vmcnt(18)" ::: "memory");
+    else if (stores >= 4) asm volatile("s_waitcnt vmcnt(14)" ::: "memory");
     else asm volatile("s_waitcnt vmcnt(10)" ::: "memory");
     asm volatile("s_barrier" ::: "memory");
 }
@@ -78,7 +78,7 @@ struct Tile256 {
     int kbytes, nst;
     int rows, cols;
     int64_t at;         // element offset of its first element in C
-    int64_t m0, n0;     // the ffn kinds: its first row and column instead
+    int64_t m0, n0;     // the forward kind: its first row and column instead
     bool none;          // and whether its rows are in no group
 };
 
@@ -169,7 +169,6 @@ __global__ __launch_bounds__(256, 1) void k_mx_tile256(MxKindArgs<KIND> args, un
                 return true;
             }
             if constexpr (KIND == kForward) zero_forward<T>(args, o.m0, o.rows, o.n0, kTile / 2, t);
-            else if constexpr (KIND == kBackward) zero_backward<T>(args, o.m0, o.rows, o.n0, o.cols, t);
             else for (int r = wid; r < o.rows; r += 4)
                 for (int k = lane; k < o.cols; k += 64) store_c(c + o.at + r * g.ldc + k, 0.0f);
         }
@@ -262,7 +261,7 @@ __global__ __launch_bounds__(256, 1) void k_mx_tile256(MxKindArgs<KIND> args, un
         read(0, Int<0>{}, n);
     });
     bool flying = false;                // the last tile's stores may still be in flight, 32 at least
-    [[maybe_unused]] int stores = 0;    // or, of the ffn kinds, that many at least
+    [[maybe_unused]] int stores = 0;    // or, of the forward kind, that many at least
 
     for (;;) {
         const bool more = advance(nxt);
@@ -346,7 +345,7 @@ __global__ __launch_bounds__(256, 1) void k_mx_tile256(MxKindArgs<KIND> args, un
         // at q ^ (r mod 8), and is stored from there, a line a row.
         uint8_t* piece = lds + kScalesAt + (buf ^ kBufs) + wid * 4096;
         const bool whole = cur.rows == kTile && cur.cols == kTile / kMxWeights<KIND>;
-        if constexpr (KIND != kProduct) {
+        if constexpr (KIND == kForward) {
             // the accumulators as they stand: the compiler would otherwise take them apart and shuffle
             // them on their way out of the loop
 #pragma unroll
@@ -354,24 +353,14 @@ __global__ __launch_bounds__(256, 1) void k_mx_tile256(MxKindArgs<KIND> args, un
 #pragma unroll
                 for (int j = 0; j < 4; ++j) asm volatile("" : "+a"(acc[i][j]));
             // what stands before the next tile's first wait: stores of this wave that it issues last
-            if constexpr (KIND == kForward) stores = !whole ? 0 : forward_stores<T>(args, 4, 2);
-            else stores = whole ? 32 : 0;
+            stores = !whole ? 0 : forward_stores<T>(args, 4, 2);
             const int64_t m0 = cur.m0 + wm * 128;
-            const int left = cur.cols - wn * (128 / kMxWeights<KIND>);
-            const int64_t c0 = cur.n0 + wn * (128 / kMxWeights<KIND>);
-            [[maybe_unused]] Kept<4> kept;      // the checkpoint's part of 32 rows, a step ahead
-            if constexpr (KIND == kBackward) kept = load_kept<4>(args, m0 + li, c0, h);
+            const int left = cur.cols - wn * 64;
+            const int64_t c0 = cur.n0 + wn * 64;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int rows = cur.rows - wm * 128 - i * 32;
-                if constexpr (KIND == kForward) {
-                    float16v gate[2] = {acc[i][0], acc[i][1]}, up[2] = {acc[i][2], acc[i][3]};
-                    forward_rows<T, ACT, 2>(args, gate, up, piece, m0 + i * 32, rows, c0, left, whole, lane);
-                } else {
-                    const Kept<4> now = kept;
-                    if (i < 3) kept = load_kept<4>(args, m0 + (i + 1) * 32 + li, c0, h);
-                    backward_rows<T, ACT, 4>(args, acc[i], now, piece, m0 + i * 32, rows, c0, left, whole, lane);
-                }
+                const float16v gate[2] = {acc[i][0], acc[i][1]}, up[2] = {acc[i][2], acc[i][3]};
+                forward_rows<T, ACT, 2>(args, gate, up, piece, m0 + i * 32, cur.rows - wm * 128 - i * 32, c0, left, whole, lane);
                 __builtin_amdgcn_sched_barrier(0);
             }
         } else {

@@ -65,17 +65,19 @@ def activation(x, act):
 
 def activation_error(x, act):
     """Bounds on the errors of a(x) and a'(x) computed in binary32 with exponential and reciprocal good to
-    2 EPS each.  y takes up to five roundings, so e^-y is off by 5 EPS |y| + 2 EPS relative, S = 1 / (1 +
-    e^-y) by that, an addition and a reciprocal: rho = (5 |y| + 5) EPS, and a by one rounding more.  In
-    a' = S + x S t y' the product takes S, t (t = 1 - S where S < 1/2: its error is at most that of S; t =
-    e^-y S otherwise: 2 rho) and y' (3 roundings) and three more: 3 rho + 8 EPS; two for the sum.  The
-    reciprocal gives normal numbers only: an S below 2^-126, the smallest of them, is 0 (so it is where e^-y
-    overflows, from 2^128 on), which changes a by less than 2^-126 |x| and a' by less than 2^-126 (1 + |x| |y'|)."""
+    2 EPS each.  y takes up to five roundings, so e^-y is off by (5 |y| + 2) EPS relative, of which S = 1 / (1 +
+    e^-y) takes the part 1 - S, and an addition and a reciprocal of its own: rho = ((1 - S) (5 |y| + 2) + 3) EPS;
+    a = x S by one rounding more.  a' = S + a t y' with t = 1 - S, which S's error S rho and a rounding of less
+    than EPS put off: |a y'| (S rho + EPS); the product's other factors and roundings rho + 6 EPS of it (a one,
+    y' three, two products); and the sum's rounding.  The reciprocal gives normal numbers only: an S below
+    2^-126, the smallest of them, is 0 (so it is where e^-y overflows, from 2^128 on), which changes a by less than
+    2^-126 |x| and a' by less than 2^-126 (1 + |x| |y'|)."""
     y, dy = exponent(x, act)
-    rho = (5 * np.abs(y) + 5) * EPS
     a, _ = activation(x, act)
     with np.errstate(over="ignore"):
         s, t = 1 / (1 + np.exp(-y)), 1 / (1 + np.exp(y))
+    rho = (t * (5 * np.abs(y) + 2) + 3) * EPS
     tiny = 2.0 ** -126 * (1 + np.abs(x))
-    part = np.abs(x * s * t * dy)
-    return np.abs(a) * (rho + EPS) + tiny, s * rho + part * (3 * rho + 8 * EPS) + (s + part) * 2 * EPS + tiny * (1 + np.abs(dy))
+    part = np.abs(a * t * dy)
+    slope = s * rho + np.abs(a * dy) * (s * rho + EPS) + part * (rho + 6 * EPS) + (s + part) * EPS
+    return np.abs(a) * (rho + EPS) + tiny, slope + tiny * (1 + np.abs(dy))

@@ -224,6 +224,30 @@ def test_gated_backward(nv, rows, cols, act):
             assert none is None and torch.equal(only, dgu)
 
 
+def test_gradients_read_every_code_and_scale(nv):
+    """Far out a(g) = g and a'(g) = 1: with dH = 1 dU is the gate's value and dG the other's, whatever its code and
+    scale, exactly but for results below 2^-126, which may be 0; a NaN scale makes its block NaN."""
+    codes = torch.arange(256, dtype=torch.uint8, device=dev())
+    codes[[127, 255]] = 0
+    codes = torch.stack([torch.full((255, 256), 0x7E, dtype=torch.uint8, device=dev()), codes.repeat(255, 1)])
+    scales = torch.arange(255, dtype=torch.uint8, device=dev())[:, None].repeat(1, 8)
+    q = nv.MX8Tensor(codes, torch.stack([torch.full_like(scales, 127), scales]), 256)
+    v = torch.from_numpy(ref.decode(codes.cpu().numpy(), q.scales.cpu().numpy())).to(dev())
+    a = nv.MXTensor(torch.full((255, 64), 0x11, dtype=torch.uint8, device=dev()), torch.full((255, 4), 127, dtype=torch.uint8, device=dev()), 128)
+    w = nv.MXTensor(torch.zeros(256, 64, dtype=torch.uint8, device=dev()), torch.full((256, 4), 127, dtype=torch.uint8, device=dev()), 128)
+    w.codes[:, 0] = 4       # 2 x 1 / 2: dH = 1
+    for nan in (False, True):
+        if nan:
+            q.scales[0, 3, 2], q.scales[1, 9, 5] = 255, 255
+            v[:, 3, 64:96], v[1, 9, 160:192] = float("nan"), float("nan")
+        for dgu, _ in (nv.mxfp8_gated_backward(torch.ones(255, 256, device=dev()), q),
+                       nv.mxfp4_gated_backward(a, w, q, out_dtype=torch.float32)):
+            for got, want in ((dgu[:, :256], v[1]), (dgu[:, 256:], v[0])):
+                fits = want.abs() < 2.0 ** 128
+                assert torch.equal(torch.isnan(got), torch.isnan(want))
+                assert ((got.double() - want).abs()[fits] <= (want.abs()[fits] < 2.0 ** -126) * 2.0 ** -126).all()
+
+
 @pytest.mark.parametrize("act", [ref.SILU, ref.GELU])
 def test_gradients_far_out(nv, act):
     """Gates at which the exponential overflows or vanishes: finite gradients, 0 or 1 in the limit."""
