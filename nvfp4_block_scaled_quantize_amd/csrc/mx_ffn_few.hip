@@ -1,0 +1,62 @@
+// mx_ffn_few.hip -- the gated feed-forward block's forward with few rows or few tiles (kernel: mx_few.h).
+#include "mx_few.h"
+
+namespace nvfp4 {
+
+template <typename XT, int MODE, int NT, int WAVES, int BLOCKS = 1>
+static int launch(const few::FfnArgs& a, int64_t units, hipStream_t st) {
+    return few::launch<float, XT, MODE, NT, WAVES, BLOCKS, kForward>(a, units, st);
+}
+
+// The tile of a dense product, as of the plain ones (mx_few.hip).
+struct FewTile {
+    int blocks, cols;
+    int64_t units, workgroups;
+};
+static FewTile few_tile(int64_t M, int64_t N) {
+    const int64_t units = (M + 15) / 16, pairs = (M + 31) / 32, tn = (N + 15) / 16;
+    if (units == 1 || units * tn <= 256) return {1, 16, units, units * tn};
+    if (pairs * tn <= 256) return {2, 16, pairs, pairs * tn};
+    return {2, 32, pairs, pairs * ((N + 31) / 32)};
+}
+template <typename XT>
+static int launch_dense(const few::FfnArgs& a, hipStream_t st) {
+    const FewTile t = few_tile(a.f.g.M, a.f.g.N);
+    if (t.cols == 32) return launch<XT, MxDense, 32, 8, 2>(a, t.units, st);
+    if (t.blocks == 2) return launch<XT, MxDense, 16, 8, 2>(a, t.units, st);
+    if (t.workgroups > 448) return launch<XT, MxDense, 16, 4>(a, t.units, st);
+    return launch<XT, MxDense, 16, 8>(a, t.units, st);
+}
+template <typename XT>
+static int launch_rows(const few::FfnArgs& a, hipStream_t st) {
+    // every group, and the rows in none, may end in a partial unit
+    const MxGArgs& g = a.f.g;
+    const int64_t busy = g.n_groups < g.M ? g.n_groups : g.M, units = g.M / 16 + busy + 1, pairs = g.M / 32 + busy + 1;
+    if (g.M > 12 * busy && pairs * ((g.N + 63) / 64) >= 448 && few::few_fits(g.kp, g.M, 2))
+        return launch<XT, MxRows, 64, 4, 2>(a, pairs, st);
+    if (units * ((g.N + 31) / 32) < 256) return launch<XT, MxRows, 16, 4>(a, units, st);
+    return launch<XT, MxRows, 32, 4>(a, units, st);
+}
+template <typename XT>
+static int launch_x(const few::FfnArgs& a, hipStream_t st) {
+    return a.f.g.n_groups ? launch_rows<XT>(a, st) : launch_dense<XT>(a, st);
+}
+
+int mx_ffn_few(const MxFArgs& f, int x_dtype, int dtype, int act, hipStream_t st) {
+    const few::FfnArgs a = {f, act, dtype == NVFP4_BF16};
+    if (!f.x) return launch_x<uint8_t>(a, st);
+    return x_dtype == NVFP4_BF16 ? launch_x<uint16_t>(a, st) : launch_x<float>(a, st);
+}
+
+bool mx_ffn_few_dense(int64_t M, int64_t N, int64_t kp) {
+    const FewTile t = few_tile(M, N);
+    return (M <= 16 || t.workgroups <= 256) && few::few_fits(kp, M, t.blocks);
+}
+
+int64_t mx_ffn_few_quantized(int64_t M, int64_t N, int64_t kp) {
+    const FewTile t = few_tile(M, N);
+    const int64_t rows = M < 16 * t.blocks ? M : 16 * t.blocks;
+    return rows * kp * (t.workgroups > 256 ? t.workgroups : 256) / 256;
+}
+
+}  // namespace nvfp4

@@ -24,6 +24,20 @@ static int launch_forward(const MxFfnArgs& f, int dtype, int act, hipStream_t st
     return mx_forward128(f, mode, dtype, act, st);
 }
 
+// What goes to the kernel for few rows.  (RULES)
+static bool few_packed(int64_t M, int64_t N, int64_t K, int64_t n_groups) {
+    const int64_t kp = mx_pad(K), busy = n_groups < M ? n_groups : M;
+    if (M <= 0 || N <= 0 || K <= 0) return false;
+    if (n_groups) return M * kp <= busy * (kp > 48 << 10 ? kp : 48 << 10) && mx_few_fits(M, kp);
+    return mx_ffn_few_dense(M, N, kp);
+}
+static bool few_fused(int64_t M, int64_t N, int64_t K, int64_t n_groups) {
+    const int64_t kp = mx_pad(K), busy = n_groups < M ? n_groups : M;
+    if (!few_packed(M, N, K, n_groups)) return false;
+    if (n_groups) return M * kp <= busy * (kp > 8192 ? kp : 8192);
+    return M <= 2 || mx_ffn_few_quantized(M, N, kp) <= 48 << 10;
+}
+
 // Extents as in mxfp4_gemm, for a product of 2 N columns.
 static bool ffn_extents(int64_t M, int64_t N, int64_t K) {
     return mx_extent(M) && mx_extent(N) && mx_extent(2 * N) && K >= 0 && K <= kMxMaxK &&
@@ -67,6 +81,8 @@ extern "C" int mxfp4_gated(const mxfp4_tensor* a, const mxfp4_tensor* w, const i
                    mx_above(scale_rule), nullptr, nullptr, nullptr, nullptr, mx_pad(N), nullptr, 0};
     if (h_copy) f.qc = h_copy->codes, f.qs = h_copy->scales;
     if (checkpoint) f.kc = checkpoint->codes, f.ks = checkpoint->scales;
+    if (!h_copy && !checkpoint && few_packed(M, N, K, n_groups))
+        return mx_ffn_few({f.g, nullptr, 0, K, 0}, 0, h_dtype, activation, (hipStream_t)stream);
     return launch_forward(f, h ? h_dtype : NVFP4_BF16, activation, (hipStream_t)stream);
 }
 
@@ -76,7 +92,7 @@ static size_t linear_code_bytes(int64_t M, int64_t K) {
 
 extern "C" size_t mxfp4_gated_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t n_groups) {
     if (!ffn_extents(M, N, K)) return 0;        // mxfp4_gated_linear refuses them
-    return M > 0 && K > 0 ? linear_code_bytes(M, K) + (size_t)(M * (mx_pad(K) / 32)) : 0;
+    return M > 0 && K > 0 && !few_fused(M, N, K, n_groups) ? linear_code_bytes(M, K) + (size_t)(M * (mx_pad(K) / 32)) : 0;
 }
 
 extern "C" int mxfp4_gated_linear(const void* x, int dtype, int64_t M, int64_t K, int64_t ld_x, int32_t scale_rule,
@@ -93,6 +109,15 @@ extern "C" int mxfp4_gated_linear(const void* x, int dtype, int64_t M, int64_t K
     if (int rc = check_result(h, h_dtype, ldh, N, used)) return rc;
     if (int rc = mx_check_tensor(w, N && K)) return rc;
     if (int rc = mx_check_groups(offsets, n_groups, M)) return rc;
+    if (x && few_fused(M, N, K, n_groups)) {
+        if (const int size = mx_dtype_size(dtype); !size) return NVFP4_ERR_DTYPE;
+        else if ((uintptr_t)x % size) return NVFP4_ERR_ALIGN;
+        if (ld_x < K) return NVFP4_ERR_SHAPE;
+        if (scale_rule != MXFP4_SCALE_FLOOR && scale_rule != MXFP4_SCALE_CEIL) return NVFP4_ERR_MODE;
+        const MxFArgs f = {{nullptr, nullptr, w->codes, w->scales, M, N, mx_pad(K), 0, h, ldh, offsets, (int)n_groups},
+                           x, ld_x, K, mx_above(scale_rule)};
+        return mx_ffn_few(f, dtype, h_dtype, activation, (hipStream_t)stream);
+    }
     const mxfp4_tensor q = {(uint8_t*)ws, (uint8_t*)ws + (need ? linear_code_bytes(M, K) : 0)};
     const mxfp4_quant_params p = {1, 0, scale_rule, NVFP4_RNE, NVFP4_RNE, 0};
     if (int rc = mxfp4_quantize(x, dtype, 1, M, K, ld_x, 0, nullptr, 0, &p, &q, nullptr, stream)) return rc;
