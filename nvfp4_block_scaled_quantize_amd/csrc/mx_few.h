@@ -16,7 +16,7 @@
 // joins wait for them, the packed 16 rows took 10.2 us.
 //
 // The gated feed-forward block's forward (KIND): columns of H instead of C, a wave's 16 of them from 16 rows of the
-// gate's weights and 16 of the up projection's.
+// gate's weights and 16 of the up projection's; or (NT = 8) eight of them from eight rows of each, as one fragment.
 #pragma once
 #include "mx_ffn.h"
 
@@ -60,9 +60,10 @@ constexpr int kFewNone = 0x7FFFFFF0;
 // XT: uint8_t (A packed), uint16_t or float (x).
 template <typename T, typename XT, int MODE, int NT, int WAVES, int BLOCKS, int KIND = kProduct>
 __global__ __launch_bounds__(64 * WAVES) void k_mx_few(typename FewKind<KIND>::Args args, unsigned tiles_n) {
-    constexpr int kThreads = 64 * WAVES, kW = kMxWeights<KIND>;
+    constexpr bool kHalves = NT == 8;       // a fragment of W is half the gate's, half the up projection's
+    constexpr int kThreads = 64 * WAVES, kW = kHalves ? 1 : kMxWeights<KIND>;
     const MxFArgs& f = few_args(args);
-    constexpr int kSubs = NT / 16, kSplit = WAVES / kSubs;      // the waves' columns and K parts
+    constexpr int kSubs = kHalves ? 1 : NT / 16, kSplit = WAVES / kSubs;      // the waves' columns and K parts
     constexpr int kRows = kFewRows * BLOCKS;
     const MxGArgs& g = f.g;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
@@ -78,7 +79,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_mx_few(typename FewKind<KIND>::A
         if (!mx_find_tile(g.offsets, g.n_groups, (int)g.M, kRows, blockIdx.x, tiles_n, tu, tn, u)) return;
         m0 = u.row0, rows = (int)u.rows;
         if (u.group == g.n_groups) steps = 0;
-        else bc += u.group * kW * g.N * pitch, bs += u.group * kW * g.N * spitch;
+        else bc += u.group * kMxWeights<KIND> * g.N * pitch, bs += u.group * kMxWeights<KIND> * g.N * spitch;
     } else {
         mx_tile_of(blockIdx.x, (unsigned)((g.M + kRows - 1) / kRows), tiles_n, tu, tn);
         m0 = (int64_t)tu * kRows;
@@ -87,14 +88,23 @@ __global__ __launch_bounds__(64 * WAVES) void k_mx_few(typename FewKind<KIND>::A
     // Loads are checked against their operand's rows by the hardware, which returns zeros beyond
     // them: with no branch around a load none is waited for before its use.
     const int64_t n0 = (int64_t)tn * NT + sub * 16;
-    const int cols = (int)(g.N - n0 < 0 ? 0 : g.N - n0 < 16 ? g.N - n0 : 16);
+    constexpr int kCols = kHalves ? 8 : 16;
+    const int cols = (int)(g.N - n0 < 0 ? 0 : g.N - n0 < kCols ? g.N - n0 : kCols);
     __amdgpu_buffer_rsrc_t wc[kW], ws[kW];
+    int wc_at = (int)(li * pitch) + q * 16, ws_at = (int)(li * spitch);
+    if constexpr (kHalves) {
+        // from the gate's first row here to the matrix's end, below 2^31 bytes; lanes without a column read none
+        wc[0] = few_buffer(bc + n0 * pitch, (2 * g.N - n0) * pitch), ws[0] = few_buffer(bs + n0 * spitch, (2 * g.N - n0) * spitch);
+        const int64_t row = (li & 7) + (li < 8 ? 0 : g.N);
+        wc_at = (li & 7) < cols ? (int)(row * pitch) + q * 16 : kFewNone - (int)pitch;
+        ws_at = (li & 7) < cols ? (int)(row * spitch) : kFewNone - (int)pitch;
+    } else {
 #pragma unroll
-    for (int j = 0; j < kW; ++j) {
-        wc[j] = few_buffer(bc + (j * g.N + n0) * pitch, cols * pitch);
-        ws[j] = few_buffer(bs + (j * g.N + n0) * spitch, cols * spitch);
+        for (int j = 0; j < kW; ++j) {
+            wc[j] = few_buffer(bc + (j * g.N + n0) * pitch, cols * pitch);
+            ws[j] = few_buffer(bs + (j * g.N + n0) * spitch, cols * spitch);
+        }
     }
-    const int wc_at = (int)(li * pitch) + q * 16, ws_at = (int)(li * spitch);
     const int s0 = steps * part / kSplit, s1 = steps * (part + 1) / kSplit;
 
     // A load of 16 rows costs the address unit as much for 4 bytes a row as for 64, so a batch's
@@ -245,12 +255,13 @@ __global__ __launch_bounds__(64 * WAVES) void k_mx_few(typename FewKind<KIND>::A
     for (int i = t; i < kRows * NT; i += kThreads) {
         const int row = i / NT, col = i % NT;
         const float* p = sums + (col >> 4) * kWave + row * 17 + (col & 15);
-        float v[kW];
+        constexpr int kOther = kHalves ? 8 : kRows * 17;        // from the gate's sum to the up projection's
+        float v[kMxWeights<KIND>];
 #pragma unroll
-        for (int k = 0; k < kW; ++k) {
-            v[k] = p[k * kRows * 17];
+        for (int k = 0; k < kMxWeights<KIND>; ++k) {
+            v[k] = p[k * kOther];
 #pragma unroll
-            for (int w = 1; w < kSplit; ++w) v[k] += p[w * kSubs * kWave + k * kRows * 17];
+            for (int w = 1; w < kSplit; ++w) v[k] += p[w * kSubs * kWave + k * kOther];
         }
         const int64_t c = (int64_t)tn * NT + col;
         if (row >= rows || c >= g.N) continue;
