@@ -235,17 +235,19 @@ template <int KIND> constexpr int kMxWeights = KIND == kForward ? 2 : 1;
 // pairs of them) touch every bank once, and a wave stores whole pieces of rows from there, 16 bytes a lane, past
 // the caches.  `whole`: all rows and columns exist, else `rows` and `left` of them.
 template <typename T, int J>
-__device__ __forceinline__ void put_rows(uint8_t* piece, const float16v (&x)[J], T* p, int64_t ld, int rows, int left,
-                                         bool whole, int lane) {
-    constexpr int kBytes = 32 * J * (int)sizeof(T) < 128 ? 32 * J * (int)sizeof(T) : 128;   // of a row at a time
-    constexpr int kN = kBytes / (int)sizeof(T), kChunks = kBytes / 16, kRows = 64 / kChunks;
+struct Rows {
+    static constexpr int kBytes = 32 * J * (int)sizeof(T) < 128 ? 32 * J * (int)sizeof(T) : 128;    // of a row at a time
+    static constexpr int kN = kBytes / (int)sizeof(T), kPasses = 32 * J / kN, kChunks = kBytes / 16, kAtOnce = 64 / kChunks;
     using Vec = typename Oct<T>::Vec;
-    const auto swizzle = [](int r) { return kChunks == 8 ? r & 7 : (r >> 1) & 3; };
-    int h = lane >> 5, lr = lane & 31, rr = lane / kChunks, q = lane % kChunks;
-    asm volatile("" : "+v"(h), "+v"(lr), "+v"(rr), "+v"(q));    // opaque: addresses are made where they are used
-    const uint8_t* from = piece + rr * kBytes + ((q ^ swizzle(rr)) << 4);
-#pragma unroll
-    for (int pass = 0; pass < 32 * J / kN; ++pass) {
+    int h, lr, rr, q;
+    __device__ explicit Rows(int lane) : h(lane >> 5), lr(lane & 31), rr(lane / kChunks), q(lane % kChunks) {
+#ifdef __HIP_DEVICE_COMPILE__
+        asm volatile("" : "+v"(h), "+v"(lr), "+v"(rr), "+v"(q));    // opaque: addresses are made where they are used
+#endif
+    }
+    __device__ static int swizzle(int r) { return kChunks == 8 ? r & 7 : (r >> 1) & 3; }
+    // Blocks into the piece.
+    __device__ __forceinline__ void put(uint8_t* piece, const float16v (&x)[J], int pass) const {
 #pragma unroll
         for (int j = 0; j < kN / 32; ++j)
 #pragma unroll
@@ -255,22 +257,36 @@ __device__ __forceinline__ void put_rows(uint8_t* piece, const float16v (&x)[J],
                 put_c4((T*)(piece + lr * kBytes + (((byte >> 4) ^ swizzle(lr)) << 4) + (byte & 15)), v[r], v[r + 1], v[r + 2],
                        v[r + 3]);
             }
+    }
+    // The piece to p.
+    __device__ __forceinline__ void store(const uint8_t* piece, T* p, int64_t ld, int pass, int rows, int left, bool whole) const {
+        const uint8_t* from = piece + rr * kBytes + ((q ^ swizzle(rr)) << 4);
         const int col = pass * kN + q * (16 / (int)sizeof(T));
         T* to = p + rr * ld + col;
         if (whole) {
 #pragma unroll
-            for (int k = 0; k < 32 / kRows; ++k) {
+            for (int k = 0; k < 32 / kAtOnce; ++k) {
                 __builtin_nontemporal_store((Vec)*(const int4v*)(from + k * 1024), (Vec*)to);
-                to += kRows * ld;
+                to += kAtOnce * ld;
             }
         } else {
 #pragma unroll 1
-            for (int k = 0; k < 32 / kRows; ++k) {
+            for (int k = 0; k < 32 / kAtOnce; ++k) {
                 const int4v v = *(const int4v*)(from + k * 1024);
-                if (rr + k * kRows < rows) store_c16<true>(to, v, left - col);
-                to += kRows * ld;
+                if (rr + k * kAtOnce < rows) store_c16<true>(to, v, left - col);
+                to += kAtOnce * ld;
             }
         }
+    }
+};
+template <typename T, int J>
+__device__ __forceinline__ void put_rows(uint8_t* piece, const float16v (&x)[J], T* p, int64_t ld, int rows, int left,
+                                         bool whole, int lane) {
+    const Rows<T, J> r(lane);
+#pragma unroll
+    for (int pass = 0; pass < r.kPasses; ++pass) {
+        r.put(piece, x, pass);
+        r.store(piece, p, ld, pass, rows, left, whole);
     }
 }
 
@@ -320,7 +336,7 @@ __device__ __forceinline__ Kept load_kept(const MxFfnArgs& f, int64_t m, int64_t
     return k;
 }
 
-// The backward's results from two blocks d of dH and the checkpoint's.
+// The backward's results from two blocks d of dH and the checkpoint's; `piece`: 12 KiB.
 template <typename T, int ACT>
 __device__ __forceinline__ void backward_rows(const MxFfnArgs& f, const float16v (&d)[2], const Kept& kept, uint8_t* piece,
                                               int64_t m0, int rows, int64_t c0, int left, bool whole, int lane) {
@@ -350,9 +366,17 @@ __device__ __forceinline__ void backward_rows(const MxFfnArgs& f, const float16v
         }
     }
     T* const p = (T*)f.g.c + m0 * f.g.ldc + c0;
-    put_rows<T, 2>(piece, dg, p, f.g.ldc, rows, left, whole, lane);
-    put_rows<T, 2>(piece, du, p + f.g.N, f.g.ldc, rows, left, whole, lane);
-    if (f.h) put_rows<T, 2>(piece, x, (T*)f.h + m0 * f.ldh + c0, f.ldh, rows, left, whole, lane);
+    T* const ph = (T*)f.h + m0 * f.ldh + c0;
+    const Rows<T, 2> r(lane);
+#pragma unroll
+    for (int pass = 0; pass < r.kPasses; ++pass) {
+        r.put(piece, dg, pass);
+        r.put(piece + 4096, du, pass);
+        if (f.h) r.put(piece + 8192, x, pass);
+        r.store(piece, p, f.g.ldc, pass, rows, left, whole);
+        r.store(piece + 4096, p + f.g.N, f.g.ldc, pass, rows, left, whole);
+        if (f.h) r.store(piece + 8192, ph, f.ldh, pass, rows, left, whole);
+    }
 }
 
 // The results of `rows` rows in no group, `width` columns from n0, by a workgroup of 256.

@@ -237,8 +237,9 @@ __global__ __launch_bounds__(256, SLOTS == 2 ? 2 : 1) void k_mx_tile128(MxKindAr
     // stages' use of it) and stores them from there, 16 bytes a lane, a row's 64 columns contiguous.
     asm volatile("s_barrier" ::: "memory");
     if constexpr (KIND != kProduct) {
-        static_assert(4 * 4096 <= tile_lds(2), "the waves' pieces fit");
-        uint8_t* piece = lds + wid * 4096;
+        constexpr int kPiece = KIND == kBackward ? 12288 : 4096;
+        static_assert(4 * kPiece <= tile_lds(2), "the waves' pieces fit");
+        uint8_t* piece = lds + wid * kPiece;
         const int64_t r0 = m0 + wm * 64, c0 = n0 + wn * (kCols / 2);
         const int rows = (int)(m1 - r0 < 64 ? m1 - r0 : 64), left = (int)(g.N - c0 < kCols ? g.N - c0 : kCols);
         const bool whole = m1 - m0 >= kSide && g.N - n0 >= kCols;
