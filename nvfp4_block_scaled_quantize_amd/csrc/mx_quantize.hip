@@ -30,30 +30,39 @@ struct MxQArgs {
     uint32_t k0, k1;                // Philox key
 };
 
-// Eight elements of x from element `at` on, of which `left` exist.  FROM8: of a checkpoint, whose rows
-// are whole blocks, rounded to bfloat16 (which changes only values below 2^-126).
+// Eight elements of x from element `at` on, of which `left` exist, in two steps: as they lie there, and as they
+// are quantized.  FROM8: codes and scale of a checkpoint, whose rows are whole blocks, then their values in
+// bfloat16 (which rounds only those below 2^-126).  Those loads have no branch around them: all of a thread's are
+// on their way before the first is decoded.
+struct Oct8 {
+    uint2v w;
+    uint32_t code;
+};
 template <bool FROM8, typename T, bool STREAM = false>
-__device__ __forceinline__ Oct<T> load_x(const MxQArgs& g, int64_t at, int64_t left) {
+__device__ __forceinline__ auto load_x(const MxQArgs& g, int64_t at, int64_t left) {
     if constexpr (!FROM8) return load_oct<T, STREAM>((const T*)g.x + at, left);
     else {
-        Oct<T> o = {};
-        if (left <= 0) return o;
+        at = left > 0 ? at : 0;
         const uint2v* p = (const uint2v*)((const uint8_t*)g.x + at);
-        uint2v w = STREAM ? __builtin_nontemporal_load(p) : *p;
-        const float s = mx8_factor(g.xs[at / kMxBlock]);
-        if (left < 8) {
-            const uint64_t keep = ((uint64_t)1 << (8 * left)) - 1;
-            w[0] &= (uint32_t)keep, w[1] &= (uint32_t)(keep >> 32);
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const Quad q = mx8_values(w[i], s);
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-                o.w[2 * i + j] = __builtin_bit_cast(uint32_t, bf16x2v{(__bf16)q.v[2 * j], (__bf16)q.v[2 * j + 1]});
-        }
-        return o;
+        return Oct8{STREAM ? __builtin_nontemporal_load(p) : *p, g.xs[at / kMxBlock]};
     }
+}
+template <typename T>
+__device__ __forceinline__ const Oct<T>& values_of(const Oct<T>& o, int64_t) { return o; }
+template <typename T>
+__device__ __forceinline__ Oct<T> values_of(const Oct8& x, int64_t left) {
+    const uint64_t keep = left >= 8 ? ~(uint64_t)0 : left > 0 ? ((uint64_t)1 << (8 * left)) - 1 : 0;
+    const uint32_t w[2] = {x.w[0] & (uint32_t)keep, x.w[1] & (uint32_t)(keep >> 32)};
+    const float s = mx8_factor(left > 0 ? x.code : 0u);
+    Oct<T> o;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const Quad q = mx8_values(w[i], s);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            o.w[2 * i + j] = __builtin_bit_cast(uint32_t, bf16x2v{(__bf16)q.v[2 * j], (__bf16)q.v[2 * j + 1]});
+    }
+    return o;
 }
 
 // Stochastic: x / s in binary32 (exact but for results below 2^-126, which round to 0 with
@@ -97,20 +106,23 @@ __global__ __launch_bounds__(256) void k_mx_rows(MxQArgs g) {
     const int64_t first = (int64_t)blockIdx.x * (256 * kRowSteps), total = g.batch * g.rows * per;
     const int64_t row0 = first / per;
     const uint32_t rem = (uint32_t)(first - row0 * per);
-    Oct<T> o[kRowSteps];
+    std::conditional_t<FROM8, Oct8, Oct<T>> x[kRowSteps];
+    [[maybe_unused]] int64_t left[kRowSteps];
 #pragma unroll
     for (int i = 0; i < kRowSteps; ++i) {
         const uint32_t at = rem + threadIdx.x + 256 * i, dr = at / per;
         const int64_t r = row0 + dr, k = (int64_t)(at - dr * per) * 8;
         const int64_t b = g.batch == 1 ? 0 : r / g.rows;
         const bool in = first + threadIdx.x + 256 * i < total;
-        o[i] = load_x<FROM8, T>(g, b * g.stride + (r - b * g.rows) * g.ld + k, in ? g.cols - k : 0);
+        left[i] = in ? g.cols - k : 0;
+        x[i] = load_x<FROM8, T>(g, b * g.stride + (r - b * g.rows) * g.ld + k, left[i]);
     }
 #pragma unroll
     for (int i = 0; i < kRowSteps; ++i) {
         const int64_t at = first + threadIdx.x + 256 * i;   // oct of the copy
-        const uint32_t code = mx_scale_code(quad_max(max_bits(o[i])), g.above);
-        const uint32_t w = codes_of<SR>(o[i], code, g.sr_row, at * 8, 0, g);
+        const Oct<T>& o = values_of<T>(x[i], left[i]);
+        const uint32_t code = mx_scale_code(quad_max(max_bits(o)), g.above);
+        const uint32_t w = codes_of<SR>(o, code, g.sr_row, at * 8, 0, g);
         if (at < total) {
             ((uint32_t*)g.rc)[at] = w;
             if ((threadIdx.x & 3) == 0) g.rs[at >> 2] = (uint8_t)code;
@@ -151,10 +163,13 @@ __global__ __launch_bounds__(256) void k_mx_tile(MxQArgs g, unsigned units, unsi
     const int64_t first = b * g.stride + (row0 + tr) * g.ld + c0 + tc * 8;
     Oct<T> o[kSteps];
     const auto load = [&](auto stream) {
+        std::conditional_t<FROM8, Oct8, Oct<T>> x[kSteps];
 #pragma unroll
         for (int i = 0; i < kSteps; ++i)
-            o[i] = load_x<FROM8, T, decltype(stream)::value>(g, first + (int64_t)i * kRowsAtOnce * g.ld,
+            x[i] = load_x<FROM8, T, decltype(stream)::value>(g, first + (int64_t)i * kRowsAtOnce * g.ld,
                                                              tr + i * kRowsAtOnce < rows ? left : 0);
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) o[i] = values_of<T>(x[i], tr + i * kRowsAtOnce < rows ? left : 0);
     };
     if (g.stream) load(std::true_type{});
     else load(std::false_type{});
