@@ -8,8 +8,12 @@
 
 namespace nvfp4 {
 
-// Which tile of the forward, in percent of a round of 256 large ones (as in mx_gemm.hip): 512 small ones take 55,
-// up to 256 of them 37, and where rows are grouped a large tile's ends cost more.  (RULE)
+// Which tile of the forward, in percent of a round of 256 large ones (the rule of mx_gemm.hip; the epilogues of 512
+// small ones run beside each other's products): 512 small ones take 55, up to 256 of them 37.  8192 x 9216 x 4096
+// 318 us against 345 with small ones, 4096 x 4096 x 8192 132 against 148, 8192 x 2048 x 2048 44 against 46; but
+// 2048 x 9216 x 4096 (576 large tiles) 115 against 92.  Where rows are grouped a large tile's ends cost a little
+// more: 32768 rows over 8 groups, 4608 x 4096, 700 against 736, 16384 over 4 groups, 2048 x 4096, 179 against 167,
+// 8191 over 15 of 16 groups, 1536 x 2048, 59 against 43.  float32 H is left to the small ones.
 static int launch_forward(const MxFfnArgs& f, int dtype, int act, hipStream_t st) {
     const MxGArgs& g = f.g;
     const int mode = g.n_groups ? MxRows : MxDense;
@@ -18,19 +22,27 @@ static int launch_forward(const MxFfnArgs& f, int dtype, int act, hipStream_t st
         if (mode == MxRows) m = (2 * g.M / side + (g.n_groups < g.M ? g.n_groups : g.M) + 1) / 2;
         return m * ((2 * g.N + side - 1) / side);
     };
-    const int64_t big = (tiles(256) + 255) / 256 * (mode == MxRows ? 125 : 100), n = tiles(128), rest = n % 512;
+    const int64_t big = (tiles(256) + 255) / 256 * (mode == MxRows ? 104 : 100), n = tiles(128), rest = n % 512;
     const int64_t small = n / 512 * 55 + (rest == 0 ? 0 : rest <= 256 ? 37 : 55);
     if (dtype == NVFP4_BF16 && big <= small) return mx_forward256(f, mode, act, st);
     return mx_forward128(f, mode, dtype, act, st);
 }
 
-// What goes to the kernel for few rows.  (RULES)
+// Whether H alone, of A packed, goes to the kernel for few rows.  Dense: up to 16 rows, or as long as no compute unit
+// gets a second workgroup (17 x 4096 x 4096, 256 workgroups, 7.5 us against 11.6 by tiles, 256 x 512 x 4096 6.6
+// against 11.2; but 77 x 4999 x 2056, 471, 11.0 against 9.3, 64 x 9216 x 4096, 576, 25 against 13).  Groups: up to 48
+// Ki elements of A a group, or a row (1536 x 2048, 17 groups: 80 rows 13.6 against 14.2, 400 over 29 groups 20.6
+// against 23.4, 800 24.9 against 24.1).
 static bool few_packed(int64_t M, int64_t N, int64_t K, int64_t n_groups) {
     const int64_t kp = mx_pad(K), busy = n_groups < M ? n_groups : M;
     if (M <= 0 || N <= 0 || K <= 0) return false;
     if (n_groups) return M * kp <= busy * (kp > 48 << 10 ? kp : 48 << 10) && mx_few_fits(M, kp);
     return mx_ffn_few_dense(M, N, kp);
 }
+// Whether x is quantized inside it: as long as that costs every workgroup less than a launch.  Dense: a workgroup's
+// elements times the workgroups a compute unit up to 48 Ki, or two rows (16 x 2048 x 2048, 32 Ki, 6.3 us
+// against 7.2 as two kernels; 64 x 4096 x 2048, 64 Ki, 10.0 against 8.7); groups: up to 8 Ki elements a group, or a row
+// (24 rows over 17 of 32 groups, 1536 x 2048, 13.0 against 15.4; 400 over 29 28.0 against 23.8).
 static bool few_fused(int64_t M, int64_t N, int64_t K, int64_t n_groups) {
     const int64_t kp = mx_pad(K), busy = n_groups < M ? n_groups : M;
     if (!few_packed(M, N, K, n_groups)) return false;

@@ -103,7 +103,7 @@ def check_forward(nv, a, w, n, got, act, rule, what):
 SIZES = [(1, 1, 1), (1, 2048, 128), (1, 33, 4096), (2, 150, 2080), (7, 65, 31), (16, 16, 32), (17, 500, 1000), (31, 32, 257),
          (32, 256, 512), (33, 129, 640), (64, 1025, 384), (65, 64, 129), (100, 100, 100), (128, 128, 256), (129, 127, 384),
          (200, 350, 1500), (255, 130, 512), (256, 255, 1024), (257, 511, 130), (300, 1, 700), (513, 257, 2500),
-         (1024, 1024, 896), (2000, 65, 4097), (2304, 1280, 1152)]
+         (1024, 1024, 896), (2000, 65, 4097), (2304, 1280, 1152), (3000, 1501, 200)]
 
 
 @pytest.mark.parametrize("M,N,K", SIZES)
@@ -157,7 +157,9 @@ def test_checkpoint_bit_for_bit(nv, M, N, K):
 GROUPED = [(1, 3, 40, 96, [0, 0, 1, 1]), (24, 8, 150, 500, spread_offsets(24, 8, 0)), (100, 3, 129, 130, [0, 33, 33, 100]),
            (600, 5, 128, 384, [0, 256, 257, 300, 600, 600]), (900, 70, 48, 160, spread_offsets(900, 70, 1)),
            (1500, 4, 260, 1000, spread_offsets(1500, 4, 2, tail=300)), (64, 2, 33, 64, [0, 0, 0]), (300, 3, 50, 64, [5, 900, 2, 300]),
-           (6000, 5, 2300, 300, [0, 2000, 2000, 2600, 2601, 5500]), (20000, 70, 1050, 200, many_offsets(20000, 70, 7, 100))]
+           (6000, 5, 2300, 300, [0, 2000, 2000, 2600, 2601, 5500]), (20000, 70, 1050, 200, many_offsets(20000, 70, 7, 100)),
+           # few groups of many rows: the forward's large tiles, one round of them and two, with rows in no group
+           (2048, 1, 3584, 200, [0, 2000]), (3840, 2, 4096, 130, [0, 1000, 3000])]
 
 
 @pytest.mark.parametrize("case", range(len(GROUPED)))
@@ -255,7 +257,7 @@ def test_backward_grouped(nv, case):
 @pytest.mark.parametrize("rule", [ref4.FLOOR, ref4.CEIL])
 def test_linear_is_quantize_then_gated(nv, dtype, rule):
     for M, N, K in [(1, 2500, 1024), (1, 31, 70), (3, 513, 3000), (16, 320, 513), (33, 350, 260), (70, 129, 128), (300, 257, 777),
-                    (2100, 150, 512), (12, 2048, 4096), (40, 96, 300)]:
+                    (2100, 150, 512), (12, 2048, 4096), (40, 96, 300), (33, 1800, 128), (64, 2200, 256), (3, 4000, 256)]:
         print(f"gated linear {M}x{N}x{K} {dtype} {rule}", flush=True)
         x = torch.randn(M, K + 3, device=dev()).to(dtype)[:, 1:1 + K]
         w = weights(nv, (2 * N,), K, 7)
@@ -268,7 +270,8 @@ def test_linear_is_quantize_then_gated(nv, dtype, rule):
 
 @pytest.mark.parametrize("M,G,N,K,off", [(1, 4, 100, 300, [0, 0, 0, 1, 1]), (24, 8, 150, 500, spread_offsets(24, 8, 0)),
                                          (40, 3, 512, 2048, [0, 13, 13, 40]), (100, 6, 640, 512, [0, 5, 40, 40, 90, 95, 97]),
-                                         (400, 17, 1024, 256, spread_offsets(400, 17, 3)), (1500, 4, 260, 1000, [0, 7, 700, 1300, 1500])])
+                                         (400, 17, 1024, 256, spread_offsets(400, 17, 3)),
+                                         (30, 6, 1500, 500, [0, 3, 3, 11, 18, 24, 29]), (1500, 4, 260, 1000, [0, 7, 700, 1300, 1500])])
 def test_linear_grouped(nv, M, G, N, K, off):
     print(f"gated linear grouped {M} {G} {N} {K}", flush=True)
     offsets = torch.tensor(off, dtype=torch.int32, device=dev())
@@ -283,6 +286,23 @@ def test_linear_grouped(nv, M, G, N, K, off):
                 pa = nv.MXTensor(a.codes[i:j].contiguous(), a.scales[i:j].contiguous(), K)
                 check_forward(nv, pa, nv.MXTensor(w.codes[e], w.scales[e], K), N, (h[i:j], None, None), ref.SILU, 0, f"group {e}")
         assert (h[ref4.spans(off, M)[-1][1]:] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_weights_past_two_gigabytes(nv, dtype):
+    """A token through 65536 rows of W of 32 KiB each: the kernel for few rows reads the two halves as two buffers."""
+    N, K = 32768, 65536
+    g = torch.Generator(device=dev()).manual_seed(51)
+    w = nv.MXTensor(torch.randint(0, 256, (2 * N, K // 2), generator=g, device=dev(), dtype=torch.uint8),
+                    torch.randint(114, 117, (2 * N, K // 32), generator=g, device=dev(), dtype=torch.uint8), K)
+    x = torch.randn(1, K, generator=g, device=dev()).to(dtype)
+    a = nv.mxfp4_quantize(x, nv.mxfp4_quant_params())[0]
+    h = nv.mxfp4_gated_linear(x, w)
+    assert torch.equal(h, nv.mxfp4_gated(a, w, out_dtype=dtype)[0])
+    some = torch.cat([torch.arange(0, 40), torch.randint(0, N, (50,)), torch.arange(N - 40, N)]).to(dev())
+    rows = torch.cat([some, some + N])
+    part = nv.MXTensor(w.codes[rows], w.scales[rows], K)
+    check_forward(nv, a, part, some.numel(), (h[:, some], None, None), ref.SILU, 0, "two gigabytes")
 
 
 @pytest.mark.parametrize("M,N,K", [(0, 5, 40), (5, 0, 40), (5, 40, 0), (300, 200, 0)])
