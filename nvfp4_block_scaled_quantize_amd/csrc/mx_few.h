@@ -17,6 +17,8 @@
 //
 // The gated feed-forward block's forward (KIND): columns of H instead of C, a wave's 16 of them from 16 rows of the
 // gate's weights and 16 of the up projection's; or (NT = 8) eight of them from eight rows of each, as one fragment.
+// 1 x 9216 x 4096 9.2 us (W, 40 MB, at the rate of plain reads 5.6, an empty kernel 2.4), 1 x 4096 x 2048 4.3,
+// 24 rows over 17 of 32 groups, 1536 x 2048 (57 MB of W), 12.8.
 #pragma once
 #include "mx_ffn.h"
 

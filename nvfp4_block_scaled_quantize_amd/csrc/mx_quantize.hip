@@ -7,6 +7,9 @@
 // Bound by memory: an element costs 2 or 4 bytes read and 17/32 written per copy.  There is no
 // pass for a tensor maximum, so every element is read once.
 //
+// From a checkpoint (FROM8) it is 33/32 bytes read: 8192 x 4096 both copies 23 to 26 us (the same of bfloat16 29), the
+// row copy 15, the column copy 16, against floors of 10, 7 and 7; 8192 x 9216 51, 31 and 33.
+//
 // Stochastic rounding of bfloat16 is bound by the vector units instead (busy in 0.84 of the
 // cycles, in 0.42 to nearest): ten Philox rounds per eight elements and copy, and a conversion
 // each.  8192 x 9216 both copies 78 us against 47 to nearest, the row copy alone 44 against 35;

@@ -18,7 +18,17 @@
 // Stages of 128 elements instead (16 rows x 64 bytes a load) took 45, 54, 20 and 8 us.
 //
 // The gated feed-forward block (KIND), forward: a tile is 128 x 64 of H; wave (wm, wn) has the gate's
-// columns 32 wn .. + 31 in its accumulator 0 and the same of the up projection in 1.  Backward: a tile of dH.
+// columns 32 wn .. + 31 in its accumulator 0 and the same of the up projection in 1.  2048 x 9216 x 4096 92 to 95
+// us (the product alone, all 18432 columns, 88 to 92), 512 x 4096 x 4096 14.
+//
+// Backward: a tile of dH, whose epilogue reads the checkpoint and writes dG, dU and H.  8192 x 9216 x 4096 280
+// us, 260 without H; 4096 x 9216 x 4096 139; 8192 x 4096 x 2048 85 (a bfloat16 dH on large tiles and a kernel that
+// reads it: 287, 160 and 104).  With nothing stored it takes 215, without the checkpoint's loads 213, without
+// the epilogue 161: what goes to and from memory (156 and 453 MB, 87 us at the rates of plain reads and
+// writes) adds to the product's time instead of hiding beside it, whichever way it is asked for.  Slower
+// or no faster: 256 x 256 tiles (291), the checkpoint loaded straight into LDS as another stage of codes (282), its
+// lines touched a tile ahead (292), loads past the caches (287), the two workgroups of a unit started half a
+// tile apart (280).
 #pragma once
 #include "mx_tile.h"
 #include "mx_ffn.h"
