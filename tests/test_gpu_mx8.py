@@ -259,3 +259,21 @@ def test_gradients_far_out(nv, act):
     pairs = on_gpu(gradients(v[0], v[1], np.ones(v[0].shape), act))
     for got, pair, what in zip((dgu[:, :32], dgu[:, 32:], h), pairs, ("dG", "dU", "H")):
         close(got, *pair, what)
+
+
+@pytest.mark.parametrize("act", [ref.SILU, ref.GELU])
+def test_gradients_at_the_ends_of_the_range(nv, act):
+    """From 2^9 on a(g) = g and a'(g) = 1, or both 0 (binary32 leaves nothing else), up to the largest g there is."""
+    g = torch.tensor([s * v for v in (512.0, 1e6, 1.5e19, 2e19, 1e30, 3e38) for s in (1, -1)], device=dev()).repeat_interleave(32)[None]
+    u = torch.full_like(g, 1.5)
+    q = nv.mxfp8_quantize(torch.stack([g, u]))
+    v = nv.mxfp8_dequantize(q)
+    a = nv.MXTensor(torch.full((1, 64), 0x11, dtype=torch.uint8, device=dev()), torch.full((1, 4), 127, dtype=torch.uint8, device=dev()), 128)
+    w = nv.MXTensor(torch.zeros(g.numel(), 64, dtype=torch.uint8, device=dev()), torch.full((g.numel(), 4), 127, dtype=torch.uint8, device=dev()), 128)
+    w.codes[:, 0] = 4       # 2 x 1 / 2: dH = 1
+    for dgu, h in (nv.mxfp8_gated_backward(torch.ones_like(g), q, activation=act, out_dtype=torch.float32, h=True),
+                   nv.mxfp4_gated_backward(a, w, q, activation=act, out_dtype=torch.float32, h=True)):
+        n = g.numel()
+        assert torch.equal(dgu[:, :n], torch.where(g > 0, 1.5, 0.0))
+        assert torch.equal(dgu[:, n:], torch.where(g > 0, v[0], 0.0))
+        assert torch.equal(h, torch.where(g > 0, 1.5 * v[0], 0.0))      # an infinity where that leaves the range
