@@ -18,7 +18,8 @@
 // The gated feed-forward block's forward (KIND): columns of H instead of C, a wave's 16 of them from 16 rows of the
 // gate's weights and 16 of the up projection's; or (NT = 8) eight of them from eight rows of each, as one fragment.
 // 1 x 9216 x 4096 9.2 us (W, 40 MB, at the rate of plain reads 5.6, an empty kernel 2.4), 1 x 4096 x 2048 4.3,
-// 24 rows over 17 of 32 groups, 1536 x 2048 (57 MB of W), 12.8.
+// 24 rows over 17 of 32 groups, 1536 x 2048 (57 MB of W), 12.8.  Its backward: a product whose last step reads
+// the checkpoint, a byte a column.
 #pragma once
 #include "mx_ffn.h"
 
@@ -28,10 +29,17 @@
 namespace nvfp4 {
 namespace few {
 
-// Activation and type of H, which only a workgroup's last step looks at, are arguments.
+// Activation and type of the results, which only a workgroup's last step looks at, are arguments; `b`: what the
+// backward reads and writes besides.
 struct FfnArgs {
     MxFArgs f;
     int act, bf16;
+    struct Backward {
+        const uint8_t *kc, *ks;
+        int64_t np;
+        void* h;
+        int64_t ldh;
+    } b;
 };
 template <int KIND> struct FewKind { using Args = FfnArgs; };
 template <> struct FewKind<kProduct> { using Args = MxFArgs; };
@@ -73,6 +81,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_mx_few(typename FewKind<KIND>::A
     const int li = lane & 15, q = lane >> 4, sub = wid % kSubs, part = wid / kSubs;
     unsigned tn, tu;
     int64_t m0 = 0;
+    [[maybe_unused]] bool none = false;     // the rows are in no group
     int rows = (int)g.M, steps = (int)(g.kp / 128);
     const int64_t pitch = g.kp / 2, spitch = g.kp / 32;
     const uint8_t *bc = g.bc, *bs = g.bs;
@@ -80,7 +89,8 @@ __global__ __launch_bounds__(64 * WAVES) void k_mx_few(typename FewKind<KIND>::A
         MxUnit u;
         if (!mx_find_tile(g.offsets, g.n_groups, (int)g.M, kRows, blockIdx.x, tiles_n, tu, tn, u)) return;
         m0 = u.row0, rows = (int)u.rows;
-        if (u.group == g.n_groups) steps = 0;
+        none = u.group == g.n_groups;
+        if (none) steps = 0;
         else bc += u.group * kMxWeights<KIND> * g.N * pitch, bs += u.group * kMxWeights<KIND> * g.N * spitch;
     } else {
         mx_tile_of(blockIdx.x, (unsigned)((g.M + kRows - 1) / kRows), tiles_n, tu, tn);
@@ -268,7 +278,21 @@ __global__ __launch_bounds__(64 * WAVES) void k_mx_few(typename FewKind<KIND>::A
         const int64_t c = (int64_t)tn * NT + col;
         if (row >= rows || c >= g.N) continue;
         if constexpr (KIND == kProduct) store_c((T*)g.c + (m0 + row) * g.ldc + c, v[0]);
-        else {
+        else if constexpr (KIND == kBackward) {
+            const FfnArgs::Backward& b = args.b;
+            const int64_t m = m0 + row, at = m * b.np + c, second = g.M * b.np;
+            const float gate = mx8_values(b.kc[at], mx8_factor(b.ks[at / 32])).v[0];
+            const float up = mx8_values(b.kc[second + at], mx8_factor(b.ks[(second + at) / 32])).v[0];
+            const Act a = args.act == MXFP4_SILU ? act_both<MXFP4_SILU>(gate) : act_both<MXFP4_GELU>(gate);
+            const float dg = none ? 0.0f : v[0] * up * a.slope, du = none ? 0.0f : v[0] * a.a, x = none ? 0.0f : a.a * up;
+            const auto put = [&](auto* p, auto* h) {
+                store_c(p + m * g.ldc + c, dg);
+                store_c(p + m * g.ldc + g.N + c, du);
+                if (h) store_c(h + m * b.ldh + c, x);
+            };
+            if (args.bf16) put((uint16_t*)g.c, (uint16_t*)b.h);
+            else put((float*)g.c, (float*)b.h);
+        } else {
             const float a = args.act == MXFP4_SILU ? act_value<MXFP4_SILU>(v[0]) : act_value<MXFP4_GELU>(v[0]);
             const int64_t at = (m0 + row) * g.ldc + c;
             if (args.bf16) store_c((uint16_t*)g.c + at, a * v[1]);

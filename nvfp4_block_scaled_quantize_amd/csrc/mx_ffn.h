@@ -418,6 +418,7 @@ int mx_backward128(const MxFfnArgs& f, int mode, int dtype, int act, hipStream_t
 // H alone for few rows or few tiles (mx_ffn_few.hip): A packed (f.x null) or quantized from x.  Whether a dense
 // product belongs there, and the elements of x that a workgroup quantizes, times the workgroups a compute unit.
 int mx_ffn_few(const MxFArgs& f, int x_dtype, int dtype, int act, hipStream_t st);
+int mx_ffn_few_backward(const MxFfnArgs& f, int64_t K, int dtype, int act, hipStream_t st);
 bool mx_ffn_few_dense(int64_t M, int64_t N, int64_t kp);
 int64_t mx_ffn_few_quantized(int64_t M, int64_t N, int64_t kp);
 inline bool mx_activation(int32_t a) { return a == MXFP4_SILU || a == MXFP4_GELU; }

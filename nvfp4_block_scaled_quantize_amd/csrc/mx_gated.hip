@@ -50,6 +50,14 @@ static bool few_fused(int64_t M, int64_t N, int64_t K, int64_t n_groups) {
     return M <= 2 || mx_ffn_few_quantized(M, N, kp) <= 48 << 10;
 }
 
+// Whether the backward goes there: the rule of the plain products.  (BACK)
+static bool few_backward(int64_t M, int64_t N, int64_t K, int64_t n_groups) {
+    const int64_t kp = mx_pad(K), busy = n_groups < M ? n_groups : M;
+    if (M <= 0 || N <= 0 || K <= 0) return false;
+    if (n_groups) return M * kp <= busy * (kp > 48 << 10 ? kp : 48 << 10) && mx_few_fits(M, kp);
+    return mx_few_dense(M, N, kp);
+}
+
 // Extents as in mxfp4_gemm, for a product of 2 N columns.
 static bool ffn_extents(int64_t M, int64_t N, int64_t K) {
     return mx_extent(M) && mx_extent(N) && mx_extent(2 * N) && K >= 0 && K <= kMxMaxK &&
@@ -153,5 +161,6 @@ extern "C" int mxfp4_gated_backward(const mxfp4_tensor* dy, const mxfp4_tensor* 
     if (!used) return NVFP4_OK;
     const MxFfnArgs f = {{dy->codes, dy->scales, w->codes, w->scales, M, N, mx_pad(K), 0, dgu, ld, offsets, (int)n_groups},
                          0, nullptr, nullptr, checkpoint->codes, checkpoint->scales, mx_pad(N), h, ldh};
+    if (few_backward(M, N, K, n_groups)) return mx_ffn_few_backward(f, K, dtype, activation, (hipStream_t)stream);
     return mx_backward128(f, n_groups ? MxRows : MxDense, dtype, activation, (hipStream_t)stream);
 }
