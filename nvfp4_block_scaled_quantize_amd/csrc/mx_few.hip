@@ -52,6 +52,7 @@ static int launch_rows(const MxFArgs& f, hipStream_t st) {
 }
 
 bool mx_few_fits(int64_t M, int64_t kp) { return few_fits(kp, M, 1); }
+bool mx_few_two_fit(int64_t M, int64_t kp) { return few_fits(kp, M, 2); }
 
 bool mx_few_dense(int64_t M, int64_t N, int64_t kp) {
     const FewTile t = few_tile(M, N);

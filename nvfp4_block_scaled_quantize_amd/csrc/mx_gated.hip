@@ -50,12 +50,17 @@ static bool few_fused(int64_t M, int64_t N, int64_t K, int64_t n_groups) {
     return M <= 2 || mx_ffn_few_quantized(M, N, kp) <= 48 << 10;
 }
 
-// Whether the backward goes there: the rule of the plain products.  (BACK)
+// Whether the backward goes there, where its epilogue costs less than on tiles.  Dense: what the plain products send,
+// or up to 800 workgroups of 32 x 32 (300 x 1500 x 1000, 470 of them, 6.2 us against 12.7, 700 x 777 x 1300, 550, 10.3
+// against 13.4, 1000 x 777 x 489, 800, 9.6 against 11.7; but 512 x 2048 x 2048, 1024, 12.7 against 11.5).  Groups: up
+// to 48 Ki elements of dY a group, or a row (400 rows over 29 groups, 1536 x 2048, 16.0 against 19.5; 600 over 15, 77
+// Ki, 15.4 against 13.7), or up to 1024 such workgroups (1000 x 600 x 700 over 6 groups, 703, 7.0 against 11.8).
 static bool few_backward(int64_t M, int64_t N, int64_t K, int64_t n_groups) {
-    const int64_t kp = mx_pad(K), busy = n_groups < M ? n_groups : M;
+    const int64_t kp = mx_pad(K), busy = n_groups < M ? n_groups : M, cols = (N + 31) / 32;
     if (M <= 0 || N <= 0 || K <= 0) return false;
-    if (n_groups) return M * kp <= busy * (kp > 48 << 10 ? kp : 48 << 10) && mx_few_fits(M, kp);
-    return mx_few_dense(M, N, kp);
+    if (n_groups)
+        return (M * kp <= busy * (kp > 48 << 10 ? kp : 48 << 10) || (M / 32 + busy) * cols <= 1024) && mx_few_fits(M, kp);
+    return mx_few_dense(M, N, kp) || ((M + 31) / 32 * cols <= 800 && mx_few_two_fit(M, kp));
 }
 
 // Extents as in mxfp4_gemm, for a product of 2 N columns.

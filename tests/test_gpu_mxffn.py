@@ -103,7 +103,7 @@ def check_forward(nv, a, w, n, got, act, rule, what):
 SIZES = [(1, 1, 1), (1, 2048, 128), (1, 33, 4096), (2, 150, 2080), (7, 65, 31), (16, 16, 32), (17, 500, 1000), (31, 32, 257),
          (32, 256, 512), (33, 129, 640), (64, 1025, 384), (65, 64, 129), (100, 100, 100), (128, 128, 256), (129, 127, 384),
          (200, 350, 1500), (255, 130, 512), (256, 255, 1024), (257, 511, 130), (300, 1, 700), (513, 257, 2500),
-         (1024, 1024, 896), (2000, 65, 4097), (2304, 1280, 1152), (3000, 1501, 200)]
+         (1024, 1024, 896), (2000, 65, 4097), (2304, 1280, 1152), (3000, 1501, 200), (2, 7200, 128), (33, 1800, 128)]
 
 
 @pytest.mark.parametrize("M,N,K", SIZES)
@@ -159,7 +159,7 @@ GROUPED = [(1, 3, 40, 96, [0, 0, 1, 1]), (24, 8, 150, 500, spread_offsets(24, 8,
            (1500, 4, 260, 1000, spread_offsets(1500, 4, 2, tail=300)), (64, 2, 33, 64, [0, 0, 0]), (300, 3, 50, 64, [5, 900, 2, 300]),
            (6000, 5, 2300, 300, [0, 2000, 2000, 2600, 2601, 5500]), (20000, 70, 1050, 200, many_offsets(20000, 70, 7, 100)),
            # few groups of many rows: the forward's large tiles, one round of them and two, with rows in no group
-           (2048, 1, 3584, 200, [0, 2000]), (3840, 2, 4096, 130, [0, 1000, 3000])]
+           (2048, 1, 3584, 200, [0, 2000]), (3840, 2, 4096, 130, [0, 1000, 3000]), (400, 17, 1024, 256, spread_offsets(400, 17, 3))]
 
 
 @pytest.mark.parametrize("case", range(len(GROUPED)))
