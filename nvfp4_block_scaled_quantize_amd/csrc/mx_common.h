@@ -137,7 +137,7 @@ template <int CTRL, int ROWS = 0xF>
 __device__ __forceinline__ int dpp(int old, int v) {
     return __builtin_amdgcn_update_dpp(old, v, CTRL, ROWS, 0xF, false);
 }
-constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kRor4 = 0x124, kRor8 = 0x128, kWaveShr1 = 0x138;
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kRor4 = 0x124, kRor8 = 0x128, kWaveShr1 = 0x138, kHalfMirror = 0x141;
 
 // Largest over the four lanes of a quad, which hold one block.
 __device__ __forceinline__ uint32_t quad_max(uint32_t m) {

@@ -7,8 +7,9 @@
 // Bound by memory: an element costs 2 or 4 bytes read and 17/32 written per copy.  There is no
 // pass for a tensor maximum, so every element is read once.
 //
-// From a checkpoint (FROM8) it is 33/32 bytes read: 8192 x 4096 both copies 23 to 26 us (the same of bfloat16 29), the
-// row copy 15, the column copy 16, against floors of 10, 7 and 7; 8192 x 9216 51, 31 and 33.
+// From a checkpoint it is 33/32 bytes read, and as many instructions as the vector units do meanwhile: 8192 x 4096
+// both copies 22 us (the same of bfloat16 29), the row copy 10, the column copy 12, against floors of 10, 7 and 7;
+// 8192 x 9216 49, 22 and 30.
 //
 // Stochastic rounding of bfloat16 is bound by the vector units instead (busy in 0.84 of the
 // cycles, in 0.42 to nearest): ten Philox rounds per eight elements and copy, and a conversion
@@ -32,41 +33,6 @@ struct MxQArgs {
     int stream;                     // read x past the caches
     uint32_t k0, k1;                // Philox key
 };
-
-// Eight elements of x from element `at` on, of which `left` exist, in two steps: as they lie there, and as they
-// are quantized.  FROM8: codes and scale of a checkpoint, whose rows are whole blocks, then their values in
-// bfloat16 (which rounds only those below 2^-126).  Those loads have no branch around them: all of a thread's are
-// on their way before the first is decoded.
-struct Oct8 {
-    uint2v w;
-    uint32_t code;
-};
-template <bool FROM8, typename T, bool STREAM = false>
-__device__ __forceinline__ auto load_x(const MxQArgs& g, int64_t at, int64_t left) {
-    if constexpr (!FROM8) return load_oct<T, STREAM>((const T*)g.x + at, left);
-    else {
-        at = left > 0 ? at : 0;
-        const uint2v* p = (const uint2v*)((const uint8_t*)g.x + at);
-        return Oct8{STREAM ? __builtin_nontemporal_load(p) : *p, g.xs[at / kMxBlock]};
-    }
-}
-template <typename T>
-__device__ __forceinline__ const Oct<T>& values_of(const Oct<T>& o, int64_t) { return o; }
-template <typename T>
-__device__ __forceinline__ Oct<T> values_of(const Oct8& x, int64_t left) {
-    const uint64_t keep = left >= 8 ? ~(uint64_t)0 : left > 0 ? ((uint64_t)1 << (8 * left)) - 1 : 0;
-    const uint32_t w[2] = {x.w[0] & (uint32_t)keep, x.w[1] & (uint32_t)(keep >> 32)};
-    const float s = mx8_factor(left > 0 ? x.code : 0u);
-    Oct<T> o;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const Quad q = mx8_values(w[i], s);
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-            o.w[2 * i + j] = __builtin_bit_cast(uint32_t, bf16x2v{(__bf16)q.v[2 * j], (__bf16)q.v[2 * j + 1]});
-    }
-    return o;
-}
 
 // Stochastic: x / s in binary32 (exact but for results below 2^-126, which round to 0 with
 // every draw that f 2^16 < 1 allows), then the conversion at unit scale.  e: the first
@@ -103,29 +69,26 @@ __device__ __forceinline__ uint32_t codes_of(const Oct<T>& o, uint32_t code, boo
 // in turn) 8192 x 9216 bfloat16 35 to 37 us, 5.5 to 5.2 TB/s read and written; 16 x 4096 2.7 us, an
 // empty kernel's time.
 constexpr int kRowSteps = 4;
-template <typename T, bool SR, bool FROM8>
+template <typename T, bool SR>
 __global__ __launch_bounds__(256) void k_mx_rows(MxQArgs g) {
     const uint32_t per = (uint32_t)(g.row_kp / 8);      // octs of a row
     const int64_t first = (int64_t)blockIdx.x * (256 * kRowSteps), total = g.batch * g.rows * per;
     const int64_t row0 = first / per;
     const uint32_t rem = (uint32_t)(first - row0 * per);
-    std::conditional_t<FROM8, Oct8, Oct<T>> x[kRowSteps];
-    [[maybe_unused]] int64_t left[kRowSteps];
+    Oct<T> o[kRowSteps];
 #pragma unroll
     for (int i = 0; i < kRowSteps; ++i) {
         const uint32_t at = rem + threadIdx.x + 256 * i, dr = at / per;
         const int64_t r = row0 + dr, k = (int64_t)(at - dr * per) * 8;
         const int64_t b = g.batch == 1 ? 0 : r / g.rows;
         const bool in = first + threadIdx.x + 256 * i < total;
-        left[i] = in ? g.cols - k : 0;
-        x[i] = load_x<FROM8, T>(g, b * g.stride + (r - b * g.rows) * g.ld + k, left[i]);
+        o[i] = load_oct((const T*)g.x + b * g.stride + (r - b * g.rows) * g.ld + k, in ? g.cols - k : 0);
     }
 #pragma unroll
     for (int i = 0; i < kRowSteps; ++i) {
         const int64_t at = first + threadIdx.x + 256 * i;   // oct of the copy
-        const Oct<T>& o = values_of<T>(x[i], left[i]);
-        const uint32_t code = mx_scale_code(quad_max(max_bits(o)), g.above);
-        const uint32_t w = codes_of<SR>(o, code, g.sr_row, at * 8, 0, g);
+        const uint32_t code = mx_scale_code(quad_max(max_bits(o[i])), g.above);
+        const uint32_t w = codes_of<SR>(o[i], code, g.sr_row, at * 8, 0, g);
         if (at < total) {
             ((uint32_t*)g.rc)[at] = w;
             if ((threadIdx.x & 3) == 0) g.rs[at >> 2] = (uint8_t)code;
@@ -140,7 +103,7 @@ __global__ __launch_bounds__(256) void k_mx_rows(MxQArgs g) {
 // that the four row blocks of 16 dword columns, which a wave reads at once (a quad of lanes
 // per column, for 64 contiguous bytes of its codes), are in different banks.  From memory 8192 x 9216
 // bfloat16 47 to 49 us, 4.9 to 4.7 TB/s; 8192 x 4608 float32 45 to 47 us, 4.2 to 4.0 TB/s.
-template <typename T, bool SR, bool FROM8>
+template <typename T, bool SR>
 __global__ __launch_bounds__(256) void k_mx_tile(MxQArgs g, unsigned units, unsigned col_tiles) {
     constexpr int kTileCols = 256 / sizeof(T), kPerRow = kTileCols / 8;   // octs of a tile row
     constexpr int kRowsAtOnce = 256 / kPerRow, kSteps = kMxPad / kRowsAtOnce;
@@ -163,16 +126,13 @@ __global__ __launch_bounds__(256) void k_mx_tile(MxQArgs g, unsigned units, unsi
     const int64_t c0 = (int64_t)ct * kTileCols;
     const int tr = t / kPerRow, tc = t % kPerRow;        // this lane's row and oct of a step
     const int64_t left = g.cols - c0 - tc * 8;
-    const int64_t first = b * g.stride + (row0 + tr) * g.ld + c0 + tc * 8;
+    const T* p = (const T*)g.x + b * g.stride + (row0 + tr) * g.ld + c0 + tc * 8;
     Oct<T> o[kSteps];
     const auto load = [&](auto stream) {
-        std::conditional_t<FROM8, Oct8, Oct<T>> x[kSteps];
 #pragma unroll
         for (int i = 0; i < kSteps; ++i)
-            x[i] = load_x<FROM8, T, decltype(stream)::value>(g, first + (int64_t)i * kRowsAtOnce * g.ld,
-                                                             tr + i * kRowsAtOnce < rows ? left : 0);
-#pragma unroll
-        for (int i = 0; i < kSteps; ++i) o[i] = values_of<T>(x[i], tr + i * kRowsAtOnce < rows ? left : 0);
+            o[i] = load_oct<T, decltype(stream)::value>(p + (int64_t)i * kRowsAtOnce * g.ld,
+                                                        tr + i * kRowsAtOnce < rows ? left : 0);
     };
     if (g.stream) load(std::true_type{});
     else load(std::false_type{});
@@ -250,6 +210,178 @@ __global__ __launch_bounds__(256) void k_mx_tile(MxQArgs g, unsigned units, unsi
         if (c < g.cols) {
             *(uint4*)(g.cc + e / 2) = make_uint4(w[0], w[1], w[2], w[3]);
             if (rb == 0) *(uint32_t*)(g.cs + e / 32) = sc;
+        }
+    }
+}
+
+// ---------------------------------------------------------------- from a checkpoint
+// A lane takes 16 elements, half a block: their codes in one load.  A checkpoint's rows are as wide as the
+// rowwise copy's, so element for element the two lie at the same index.  The conversion takes the block's scale
+// and gives bfloat16, rounded only below 2^-126; with scale code 255 every code gives NaN.  (Row copy of 8192 x 4096
+// 10 us against 15 with eight elements a lane, conversions by way of binary32 and the rows' divisions.)
+struct Kept16 {
+    int4v w;
+    uint32_t code;
+};
+template <bool STREAM>
+__device__ __forceinline__ Kept16 load_kept16(const MxQArgs& g, int64_t at) {
+    const int4v* p = (const int4v*)((const uint8_t*)g.x + at);
+    return {STREAM ? __builtin_nontemporal_load(p) : *p, g.xs[at / kMxBlock]};
+}
+// Zeros in place of all but the first `left` elements.
+__device__ __forceinline__ void keep16(Kept16& x, int64_t left) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (left < 4 * i + 4) x.w[i] = left <= 4 * i ? 0 : x.w[i] & ((1 << (8 * (left - 4 * i))) - 1);
+    if (left <= 0) x.code = 0;
+}
+struct Oct16 {
+    Oct<uint16_t> o[2];
+};
+__device__ __forceinline__ uint32_t kept_pair(uint32_t w, float s, bool upper) {
+    return upper ? __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, true))
+                 : __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, false));
+}
+__device__ __forceinline__ Oct16 values_of(const Kept16& x) {
+    const float s = mx8_factor(x.code);
+    Oct16 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        v.o[i / 2].w[i % 2 * 2] = kept_pair(x.w[i], s, false), v.o[i / 2].w[i % 2 * 2 + 1] = kept_pair(x.w[i], s, true);
+    return v;
+}
+__device__ __forceinline__ uint32_t pair_scale(const Oct16& v, uint32_t above) {
+    const uint32_t m = max(max_bits(v.o[0]), max_bits(v.o[1]));
+    return mx_scale_code(max(m, (uint32_t)dpp<kXor1>(0, (int)m)), above);
+}
+// The bits of four lane pairs' values, of eight lanes.
+__device__ __forceinline__ uint32_t join8(uint32_t v) {
+    v |= (uint32_t)dpp<kXor2>(0, (int)v);
+    return v | (uint32_t)dpp<kHalfMirror>(0, (int)v);
+}
+
+template <bool SR>
+__global__ __launch_bounds__(256) void k_mx8_rows(MxQArgs g) {
+    const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x, total = g.batch * g.rows * (g.row_kp / 16);
+    const int64_t from = (at < total ? at : total - 1) * 16;
+    Kept16 x = g.stream ? load_kept16<true>(g, from) : load_kept16<false>(g, from);
+    if (g.cols < g.row_kp) {
+        const uint32_t per = (uint32_t)(g.row_kp / 16), rem = (uint32_t)((int64_t)blockIdx.x * 256 % per);
+        keep16(x, g.cols - (int64_t)((rem + threadIdx.x) % per) * 16);
+    }
+    const Oct16 v = values_of(x);
+    const uint32_t code = pair_scale(v, g.above);
+    const uint32_t w0 = codes_of<SR>(v.o[0], code, g.sr_row, at * 16, 0, g);
+    const uint32_t w1 = codes_of<SR>(v.o[1], code, g.sr_row, at * 16 + 8, 0, g);
+    if (at < total) {
+        ((uint2*)g.rc)[at] = make_uint2(w0, w1);
+        if ((threadIdx.x & 1) == 0) g.rs[at >> 1] = (uint8_t)code;
+    }
+}
+
+// Both copies, or the columnwise one: a workgroup takes 128 rows x 128 columns.  LDS holds the codes as they came, and
+// the blocks' scales as factors; a thread takes four columns of 16 rows, eight lanes a column's 128.  Byte c of row r
+// lies at c ^ 32 (r / 32), so that the four row blocks are in different banks.  18 KB, so that eight workgroups run
+// at once on a compute unit: 8192 x 4096 22 us against 25 with the values in LDS, 32 KB, and eight elements a lane.  Without
+// the columns' stores 16; those past the caches it takes 17, but decodes of both copies after it 5 more than they save.
+constexpr int kKeptStride = kMxPad + 4;
+template <bool SR>
+__global__ __launch_bounds__(256, 8) void k_mx8_tile(MxQArgs g, unsigned units, unsigned col_tiles) {
+    constexpr int kSteps = 4;
+    __shared__ __attribute__((aligned(16))) uint8_t tile[kMxPad * 128];
+    __shared__ __attribute__((aligned(16))) float factors[4 * kKeptStride];
+    const int t = threadIdx.x;
+    unsigned u, ct;
+    int64_t b = 0, row0, rows, kp0;
+    bool has_col = true;
+    if (g.n_groups) {
+        MxUnit m;
+        if (!mx_find_tile(g.offsets, g.n_groups, (int)g.rows, kMxPad, blockIdx.x, col_tiles, u, ct, m)) return;
+        row0 = m.row0, rows = m.rows, kp0 = (int64_t)u * kMxPad;
+        has_col = m.group != g.n_groups;
+    } else {
+        mx_tile_of(blockIdx.x, units * (unsigned)g.batch, col_tiles, u, ct);
+        b = u / units, u = u % units;
+        row0 = kp0 = (int64_t)u * kMxPad;
+        rows = g.rows - row0 < kMxPad ? g.rows - row0 : kMxPad;
+    }
+    const int64_t c0 = (int64_t)ct * 128;
+    const int tr = t >> 3, tc = t & 7;      // this lane's row and 16 columns of a step
+    const int64_t first = (b * g.rows + row0) * g.row_kp + c0 + tc * 16;
+    Kept16 x[kSteps];
+    const auto load = [&](auto stream) {
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            const int r = tr + 32 * i;
+            x[i] = load_kept16<decltype(stream)::value>(g, first + (r < rows ? r : 0) * g.row_kp);
+        }
+    };
+    if (g.stream) load(std::true_type{});
+    else load(std::false_type{});
+    if (rows < kMxPad || c0 + 128 > g.cols) {
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) keep16(x[i], tr + 32 * i < rows ? g.cols - c0 - tc * 16 : 0);
+    }
+    if (has_col) {
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            const int r = tr + 32 * i;
+            *(int4v*)(tile + r * 128 + ((tc * 16) ^ (32 * i))) = x[i].w;
+            if ((tc & 1) == 0) factors[(tc >> 1) * kKeptStride + r] = mx8_factor(x[i].code);
+        }
+    }
+    if (g.rc) {
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            const int r = tr + 32 * i;
+            const Oct16 v = values_of(x[i]);
+            const uint32_t code = pair_scale(v, g.above);
+            const int64_t e = first + r * g.row_kp;
+            const uint32_t w0 = codes_of<SR>(v.o[0], code, g.sr_row, e, 0, g);
+            const uint32_t w1 = codes_of<SR>(v.o[1], code, g.sr_row, e + 8, 0, g);
+            const uint32_t sc = join8(code << (8 * (tc >> 1)));
+            if (r < rows) {
+                *(uint2*)(g.rc + e / 2) = make_uint2(w0, w1);
+                if (tc == 0) *(uint32_t*)(g.rs + e / 32) = sc;
+            }
+        }
+    }
+    if (!has_col) return;
+    __syncthreads();
+    // columns 4 dc .. 4 dc + 3, rows 16 h .. 16 h + 15
+    const int h = t & 7, dc = t >> 3, rb = h >> 1;
+    const uint8_t* s = tile + h * 16 * 128 + ((dc * 4) ^ (32 * rb));
+    const float* f = factors + (dc >> 3) * kKeptStride + h * 16;
+    uint32_t d[2][16], m[2] = {};
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        const uint32_t w = *(const uint32_t*)(s + j * 128);
+        d[0][j] = kept_pair(w, f[j], false), d[1][j] = kept_pair(w, f[j], true);
+    }
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) m[p] = max_bf16x2(m[p], d[p][j] & 0x7FFF7FFFu);
+        m[p] = max_bf16x2(m[p], (uint32_t)dpp<kXor1>(0, (int)m[p]));
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const uint32_t* v = d[q >> 1];
+        const uint32_t code = mx_scale_code(q & 1 ? m[q >> 1] & 0xFFFF0000u : m[q >> 1] << 16, g.above);
+        const int64_t c = c0 + dc * 4 + q, e = (b * g.cols + c) * g.col_kp + kp0 + h * 16;
+        uint32_t w[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            Oct<uint16_t> o;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                o.w[j] = __builtin_amdgcn_perm(v[8 * k + 2 * j + 1], v[8 * k + 2 * j], q & 1 ? 0x07060302u : 0x05040100u);
+            w[k] = codes_of<SR>(o, code, g.sr_col, e + 8 * k, 1, g);
+        }
+        const uint32_t sc = join8(code << (8 * rb));
+        if (c < g.cols) {
+            *(uint2*)(g.cc + e / 2) = make_uint2(w[0], w[1]);
+            if (h == 0) *(uint32_t*)(g.cs + e / 32) = sc;
         }
     }
 }
@@ -372,20 +504,35 @@ static int launch_decode(const MxDArgs& g, hipStream_t st) {
     return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
 }
 
-template <typename T, bool SR, bool FROM8 = false>
+template <typename T, bool SR>
 static int launch_quantize(const MxQArgs& g, hipStream_t st) {
     if (!g.cc) {
         const int per = 256 * kRowSteps;
         const __int128 grid = ((__int128)g.batch * g.rows * (g.row_kp / 8) + per - 1) / per;
         if (!mx_grid_fits(grid, 256)) return NVFP4_ERR_SHAPE;
-        k_mx_rows<T, SR, FROM8><<<dim3((unsigned)grid), 256, 0, st>>>(g);
+        k_mx_rows<T, SR><<<dim3((unsigned)grid), 256, 0, st>>>(g);
     } else {
         // units cover the rows in no group too (one more partial unit at most); tiles cover the
         // rowwise copy's padding
         const int64_t units = g.col_kp / kMxPad, col_tiles = g.row_kp * (int64_t)sizeof(T) / 256;
         const __int128 grid = (g.n_groups ? units + 1 : (__int128)units * g.batch) * col_tiles;
         if (!mx_grid_fits(grid, 256)) return NVFP4_ERR_SHAPE;
-        k_mx_tile<T, SR, FROM8><<<dim3((unsigned)grid), 256, 0, st>>>(g, (unsigned)units, (unsigned)col_tiles);
+        k_mx_tile<T, SR><<<dim3((unsigned)grid), 256, 0, st>>>(g, (unsigned)units, (unsigned)col_tiles);
+    }
+    return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
+}
+
+template <bool SR>
+static int launch_kept(const MxQArgs& g, hipStream_t st) {
+    if (!g.cc) {
+        const __int128 grid = ((__int128)g.batch * g.rows * (g.row_kp / 16) + 255) / 256;
+        if (!mx_grid_fits(grid, 256)) return NVFP4_ERR_SHAPE;
+        k_mx8_rows<SR><<<dim3((unsigned)grid), 256, 0, st>>>(g);
+    } else {
+        const int64_t units = g.col_kp / kMxPad, col_tiles = g.row_kp / 128;
+        const __int128 grid = (g.n_groups ? units + 1 : (__int128)units * g.batch) * col_tiles;
+        if (!mx_grid_fits(grid, 256)) return NVFP4_ERR_SHAPE;
+        k_mx8_tile<SR><<<dim3((unsigned)grid), 256, 0, st>>>(g, (unsigned)units, (unsigned)col_tiles);
     }
     return hipGetLastError() == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP;
 }
@@ -467,11 +614,9 @@ extern "C" int mxfp8_to_mxfp4(const mxfp8_tensor* q, int64_t batch, int64_t rows
     if (int rc = check_copies(g, batch, rows, cols, offsets, n_groups, p, row_out, col_out, &used)) return rc;
     if (int rc = mx8_check_tensor(q, used)) return rc;
     if (!used) return NVFP4_OK;
-    g.x = q->codes, g.xs = q->scales, g.ld = mx_pad(cols);
-    g.stride = (int64_t)((uint64_t)rows * (uint64_t)g.ld);      // (a product past 64 bits is refused with the grid)
-    g.stream = (__int128)batch * rows * g.ld >= ((int64_t)128 << 20);       // as in mxfp4_quantize
-    const hipStream_t st = (hipStream_t)stream;
-    return stochastic(g) ? launch_quantize<uint16_t, true, true>(g, st) : launch_quantize<uint16_t, false, true>(g, st);
+    g.x = q->codes, g.xs = q->scales;
+    g.stream = (__int128)batch * rows * g.row_kp >= ((int64_t)128 << 20);   // as in mxfp4_quantize
+    return stochastic(g) ? launch_kept<true>(g, (hipStream_t)stream) : launch_kept<false>(g, (hipStream_t)stream);
 }
 
 extern "C" int mxfp4_dequantize(const mxfp4_tensor* q, int64_t n, int64_t k, const int32_t* offsets,
