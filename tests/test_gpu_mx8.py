@@ -161,6 +161,22 @@ def test_to_mxfp4_past_the_caches(nv):
     assert all(equal_copies(a, b) for a, b in zip(got, want))
 
 
+@pytest.mark.parametrize("nan", [False, True])
+def test_to_mxfp4_of_every_code_and_scale(nv, nan):
+    """Scale r in row r, and so 32 neighbouring ones in a columnwise block; shuffled rows in a second matrix."""
+    codes = torch.arange(256, dtype=torch.uint8).repeat(256, 1)
+    if not nan:
+        codes[(codes & 0x7F) == 0x7F] = 0
+    scales = torch.arange(256, dtype=torch.uint8)[:, None].repeat(1, 8)
+    order = torch.randperm(256, generator=torch.Generator().manual_seed(1))
+    q = nv.MX8Tensor(torch.stack([codes, codes[order][:, order]]).to(dev()), torch.stack([scales, scales[order]]).to(dev()), 256)
+    for rule in (ref4.FLOOR, ref4.CEIL):
+        for sr in (nv.NVFP4_RNE, nv.NVFP4_SR):
+            p = nv.mxfp4_quant_params(True, True, rule, sr, sr, 9)
+            got, want = nv.mxfp8_to_mxfp4(q, p), nv.mxfp4_quantize(nv.mxfp8_dequantize(q, torch.bfloat16), p)
+            assert all(equal_copies(a, b) for a, b in zip(got, want))
+
+
 def test_special_scales_reach_their_block(nv):
     x = torch.randn(40, 100, device=dev())
     x[7, 40] = float("nan")
