@@ -54,7 +54,10 @@ static bool few_fused(int64_t M, int64_t N, int64_t K, int64_t n_groups) {
 // or up to 800 workgroups of 32 x 32 (300 x 1500 x 1000, 470 of them, 6.2 us against 12.7, 700 x 777 x 1300, 550, 10.3
 // against 13.4, 1000 x 777 x 489, 800, 9.6 against 11.7; but 512 x 2048 x 2048, 1024, 12.7 against 11.5).  Groups: up
 // to 48 Ki elements of dY a group, or a row (400 rows over 29 groups, 1536 x 2048, 16.0 against 19.5; 600 over 15, 77
-// Ki, 15.4 against 13.7), or up to 1024 such workgroups (1000 x 600 x 700 over 6 groups, 703, 7.0 against 11.8).
+// Ki, 15.4 against 13.7), or up to 1024 such workgroups (1000 x 600 x 700 over 6 groups, 703, 7.0 against 11.8).  Longer
+// rows gain less: 512 x 1024 x 8192, 512 of them, 19.8 against 21.7, 1000 x 800 over 6 groups, 925, K = 1024 9.8
+// against 12.1, K = 4096 18.7 against 17.6.  (The forward on as few of these in groups wins at short rows alone: 3000 x
+// 100 x 300 over 10 5.2 against 6.7, 5000 x 64 x 4096 over 12 18.1 against 12.3.)
 static bool few_backward(int64_t M, int64_t N, int64_t K, int64_t n_groups) {
     const int64_t kp = mx_pad(K), busy = n_groups < M ? n_groups : M, cols = (N + 31) / 32;
     if (M <= 0 || N <= 0 || K <= 0) return false;
