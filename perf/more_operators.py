@@ -173,8 +173,8 @@ def prepare(case, seed):
         s["w2"] = _pack(s["w2"])
     if kind == "backward":
         s["gu"] = _pack8(s["gu"])
-        if case["out"]:                 # the columnwise copy: W2^T in blocks along its rows
-            s["w2"] = _pack(s["w2"].transpose(-1, -2))
+        if case["out"]:                 # the columnwise copy: W2^T in blocks along its rows, rows side by side
+            s["w2"] = tuple(t.contiguous() for t in _pack(s["w2"].transpose(-1, -2)))
     if kind == "reuse":
         s["x8"] = _pack8(s.pop("x"))
     return s
@@ -355,10 +355,8 @@ def _library(s):
     if not case["out"]:
         return list(nv.mxfp8_gated_backward(s["dh"], kept, activation=act, h=True))
     dy, _ = nv.mxfp4_quantize(s["dy"], p)
-    if "w2_copy" not in s:      # the calls take contiguous copies: the layer's weights are laid out once
-        s["w2_copy"] = nv.MXTensor(*(t.contiguous() for t in s["w2"]), case["out"])
-    return list(nv.mxfp4_gated_backward(dy, s["w2_copy"], kept, offsets=offsets, activation=act,
-                                        out_dtype=dtype, h=True))
+    return list(nv.mxfp4_gated_backward(dy, nv.MXTensor(*s["w2"], case["out"]), kept, offsets=offsets,
+                                        activation=act, out_dtype=dtype, h=True))
 
 
 def run(state):
