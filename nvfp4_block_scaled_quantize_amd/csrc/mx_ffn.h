@@ -61,15 +61,16 @@ template <int ACT>
 __device__ __forceinline__ float act_value(float x) {
     return x * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(act_arg<ACT>(x)));
 }
-// a(x) and a'(x) = S + x S (1 - S) y', y' = 1 or 2 z'.  The difference 1 - S is off by half a step of 1 or
-// less, which against a' near 1 is |x y'| such steps.  (x^2 is kept finite, for the product with 1 - S = 0.)
+// a(x) and a'(x) = S + x S T y', T = 1 - S = 2^-y S, y' = 1 or 2 z'.  (The difference 1 - S would leave T off by a
+// step of 1, which against a' near 1 is |x y'| of them.)  2^-y is kept finite, for the product with S = 0, where a(x)
+// is 0 and T does not matter; x^2 for the one with T = 0.
 struct Act {
     float a, slope;
 };
 template <int ACT>
 __device__ __forceinline__ Act act_both(float x) {
-    const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(act_arg<ACT>(x)));
-    const float t = 1.0f - s, a = x * s;
+    const float e = fminf(__builtin_amdgcn_exp2f(act_arg<ACT>(x)), 3.402823466e38f), s = __builtin_amdgcn_rcpf(1.0f + e);
+    const float t = e * s, a = x * s;
     if constexpr (ACT == MXFP4_SILU) return {a, __builtin_fmaf(a, t, s)};
     else return {a, __builtin_fmaf(a * t, __builtin_fmaf(6.0f * kGeluB, fminf(x * x, 1e30f), 2.0f * kGeluA), s)};
 }
