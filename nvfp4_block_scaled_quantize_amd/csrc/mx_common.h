@@ -321,9 +321,10 @@ struct MxFArgs {
 // A packed, or quantized from x; dense or grouped.
 int mx_few_packed(const MxFArgs& f, int c_dtype, hipStream_t st);
 int mx_few_linear(const MxFArgs& f, int x_dtype, int c_dtype, hipStream_t st);
-// Whether 16 rows of A, or 32, fit into a workgroup's LDS, and whether a dense product of A packed belongs
-// here: up to 16 rows, or no more than two workgroups (of 32 x 32) a compute unit.
-bool mx_few_fits(int64_t M, int64_t kp);
+// Whether it can take a grouped product (16 rows of A fit into a workgroup's LDS, and a launch takes the workgroups),
+// whether 32 rows of A fit, and whether a dense product of A packed belongs here: up to 16 rows, or no more than two
+// workgroups (of 32 x 32) a compute unit.
+bool mx_few_rows(int64_t M, int64_t N, int64_t kp, int64_t n_groups);
 bool mx_few_two_fit(int64_t M, int64_t kp);
 bool mx_few_dense(int64_t M, int64_t N, int64_t kp);
 // Elements of x that a workgroup of a dense product quantizes, times the workgroups a compute unit.

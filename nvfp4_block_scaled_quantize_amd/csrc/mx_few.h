@@ -57,6 +57,31 @@ inline int64_t few_lds(int64_t kp, int64_t M, int waves, int blocks, int weights
     return a > sums ? a : sums;
 }
 inline bool few_fits(int64_t kp, int64_t M, int blocks) { return few_lds(kp, M, 8, blocks) <= kMxMaxLds; }
+// Whether a launch can count that many workgroups, of four waves each: the eight of others are for few of them.
+inline bool few_launches(int64_t workgroups) { return mx_grid_fits(workgroups, 256); }
+
+// The tile of a grouped product: four waves on 16 rows and 32 columns, two of them sharing K (80 packed
+// rows over 17 groups, 4096 x 2048: 14.2 us against 16.4 with 16 columns and 15.4 with 64, which need no
+// split), or on 16 columns where 32 would leave compute units without work (4 rows over 4 groups, 1024 x
+// 2048: 3.3 us against 3.8), or on 32 rows and 64 columns, without a split, where the groups have
+// more than about 12 rows (400 packed rows over 17 groups 17.8 us against 23.6; 200 rows 16.4
+// either way) and there are workgroups for all compute units (1000 rows of x, 4096 x 128 over 16
+// groups 12.8 against 23.5, 200 packed rows, 2048 x 256 over 8 groups, 480 of them, 4.6 against
+// 4.9; but 100 of 1024 x 2048 over 8 groups, 192 of them, 6.7 against 5.8, 400 of x, 512 x 384 over
+// 30, 344, 5.8 against 5.1). The rule is the same for A packed and x, so that both add their sums
+// in the same order.
+struct RowsTile {
+    int blocks, cols;
+    int64_t units, workgroups;
+};
+inline RowsTile rows_tile(int64_t M, int64_t N, int64_t kp, int64_t n_groups) {
+    // every group, and the rows in none, may end in a partial unit
+    const int64_t busy = n_groups < M ? n_groups : M, units = M / 16 + busy + 1, pairs = M / 32 + busy + 1;
+    const auto tile = [&](int blocks, int cols, int64_t n) -> RowsTile { return {blocks, cols, n, n * ((N + cols - 1) / cols)}; };
+    if (M > 12 * busy && pairs * ((N + 63) / 64) >= 448 && few_fits(kp, M, 2)) return tile(2, 64, pairs);
+    if (units * ((N + 31) / 32) < 256) return tile(1, 16, units);
+    return tile(1, 32, units);
+}
 
 // At most 16 rows of an operand; an offset past them, kFewNone for one, reads as zeros.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t few_buffer(const uint8_t* p, int64_t bytes) {

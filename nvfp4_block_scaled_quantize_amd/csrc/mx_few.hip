@@ -30,33 +30,22 @@ static int launch_dense(const MxFArgs& f, hipStream_t st) {
     return launch<T, XT, MxDense, 16, 8>(f, t.units, st);
 }
 
-// Grouped: four waves on 16 rows and 32 columns, two of them sharing K (80 packed rows over 17
-// groups, 4096 x 2048: 14.2 us against 16.4 with 16 columns and 15.4 with 64, which need no split),
-// or on 16 columns where 32 would leave compute units without work (4 rows over 4 groups, 1024 x
-// 2048: 3.3 us against 3.8), or on 32 rows and 64 columns, without a split, where the groups have
-// more than about 12 rows (400 packed rows over 17 groups 17.8 us against 23.6; 200 rows 16.4
-// either way) and there are workgroups for all compute units (1000 rows of x, 4096 x 128 over 16
-// groups 12.8 against 23.5, 200 packed rows, 2048 x 256 over 8 groups, 480 of them, 4.6 against
-// 4.9; but 100 of 1024 x 2048 over 8 groups, 192 of them, 6.7 against 5.8, 400 of x, 512 x 384 over
-// 30, 344, 5.8 against 5.1). The rule is the same for A packed and x, so that both add their sums
-// in the same order.
 template <typename T, typename XT>
 static int launch_rows(const MxFArgs& f, hipStream_t st) {
-    // every group, and the rows in none, may end in a partial unit
-    const int64_t busy = f.g.n_groups < f.g.M ? f.g.n_groups : f.g.M, units = f.g.M / 16 + busy + 1;
-    const int64_t pairs = f.g.M / 32 + busy + 1;
-    if (f.g.M > 12 * busy && pairs * ((f.g.N + 63) / 64) >= 448 && few_fits(f.g.kp, f.g.M, 2))
-        return launch<T, XT, MxRows, 64, 4, 2>(f, pairs, st);
-    if (units * ((f.g.N + 31) / 32) < 256) return launch<T, XT, MxRows, 16, 4>(f, units, st);
-    return launch<T, XT, MxRows, 32, 4>(f, units, st);
+    const RowsTile t = rows_tile(f.g.M, f.g.N, f.g.kp, f.g.n_groups);
+    if (t.cols == 64) return launch<T, XT, MxRows, 64, 4, 2>(f, t.units, st);
+    if (t.cols == 16) return launch<T, XT, MxRows, 16, 4>(f, t.units, st);
+    return launch<T, XT, MxRows, 32, 4>(f, t.units, st);
 }
 
-bool mx_few_fits(int64_t M, int64_t kp) { return few_fits(kp, M, 1); }
+bool mx_few_rows(int64_t M, int64_t N, int64_t kp, int64_t n_groups) {
+    return few_fits(kp, M, 1) && few_launches(rows_tile(M, N, kp, n_groups).workgroups);
+}
 bool mx_few_two_fit(int64_t M, int64_t kp) { return few_fits(kp, M, 2); }
 
 bool mx_few_dense(int64_t M, int64_t N, int64_t kp) {
     const FewTile t = few_tile(M, N);
-    return (M <= 16 || t.workgroups <= 512) && few_fits(kp, M, t.blocks);
+    return (M <= 16 || t.workgroups <= 512) && few_fits(kp, M, t.blocks) && few_launches(t.workgroups);
 }
 
 int64_t mx_few_quantized(int64_t M, int64_t N, int64_t kp) {

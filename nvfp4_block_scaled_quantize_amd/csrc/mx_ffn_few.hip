@@ -37,13 +37,11 @@ static int launch_dense(const few::FfnArgs& a, hipStream_t st) {
 }
 template <int KIND, typename XT>
 static int launch_rows(const few::FfnArgs& a, hipStream_t st) {
-    // every group, and the rows in none, may end in a partial unit
     const MxGArgs& g = a.f.g;
-    const int64_t busy = g.n_groups < g.M ? g.n_groups : g.M, units = g.M / 16 + busy + 1, pairs = g.M / 32 + busy + 1;
-    if (g.M > 12 * busy && pairs * ((g.N + 63) / 64) >= 448 && few::few_fits(g.kp, g.M, 2))
-        return launch<KIND, XT, MxRows, 64, 4, 2>(a, pairs, st);
-    if (units * ((g.N + 31) / 32) < 256) return launch<KIND, XT, MxRows, 16, 4>(a, units, st);
-    return launch<KIND, XT, MxRows, 32, 4>(a, units, st);
+    const few::RowsTile t = few::rows_tile(g.M, g.N, g.kp, g.n_groups);
+    if (t.cols == 64) return launch<KIND, XT, MxRows, 64, 4, 2>(a, t.units, st);
+    if (t.cols == 16) return launch<KIND, XT, MxRows, 16, 4>(a, t.units, st);
+    return launch<KIND, XT, MxRows, 32, 4>(a, t.units, st);
 }
 template <int KIND, typename XT>
 static int launch_x(const few::FfnArgs& a, hipStream_t st) {
@@ -63,7 +61,7 @@ int mx_ffn_few_backward(const MxFfnArgs& f, int64_t K, int dtype, int act, hipSt
 
 bool mx_ffn_few_dense(int64_t M, int64_t N, int64_t kp) {
     const FewTile t = few_tile<kForward>(M, N, kp);
-    return (M <= 16 || t.workgroups <= 256) && few::few_fits(kp, M, t.blocks);
+    return (M <= 16 || t.workgroups <= 256) && few::few_fits(kp, M, t.blocks) && few::few_launches(t.workgroups);
 }
 
 int64_t mx_ffn_few_quantized(int64_t M, int64_t N, int64_t kp) {

@@ -36,7 +36,7 @@ static int launch_forward(const MxFfnArgs& f, int dtype, int act, hipStream_t st
 static bool few_packed(int64_t M, int64_t N, int64_t K, int64_t n_groups) {
     const int64_t kp = mx_pad(K), busy = n_groups < M ? n_groups : M;
     if (M <= 0 || N <= 0 || K <= 0) return false;
-    if (n_groups) return M * kp <= busy * (kp > 48 << 10 ? kp : 48 << 10) && mx_few_fits(M, kp);
+    if (n_groups) return M * kp <= busy * (kp > 48 << 10 ? kp : 48 << 10) && mx_few_rows(M, N, kp, n_groups);
     return mx_ffn_few_dense(M, N, kp);
 }
 // Whether x is quantized inside it: as long as that costs every workgroup less than a launch.  Dense: a workgroup's
@@ -62,7 +62,7 @@ static bool few_backward(int64_t M, int64_t N, int64_t K, int64_t n_groups) {
     const int64_t kp = mx_pad(K), busy = n_groups < M ? n_groups : M, cols = (N + 31) / 32;
     if (M <= 0 || N <= 0 || K <= 0) return false;
     if (n_groups)
-        return (M * kp <= busy * (kp > 48 << 10 ? kp : 48 << 10) || (M / 32 + busy) * cols <= 1024) && mx_few_fits(M, kp);
+        return (M * kp <= busy * (kp > 48 << 10 ? kp : 48 << 10) || (M / 32 + busy) * cols <= 1024) && mx_few_rows(M, N, kp, n_groups);
     return mx_few_dense(M, N, kp) || ((M + 31) / 32 * cols <= 800 && mx_few_two_fit(M, kp));
 }
 

@@ -98,7 +98,7 @@ extern "C" int mxfp4_gemm_grouped(const mxfp4_tensor* a, const mxfp4_tensor* b, 
     // groups: 80 rows 14.2 us against 19.8, 400 rows 17.8 against 20.2; 2048 x 6144, 8 groups: 16 rows
     // 11.4 against 15.0; 9216 x 4096, 4 groups: 32 rows 17.3 against 19.3, 64 rows (64 Ki a group)
     // 21.2 against 19.5).
-    if (K > 0 && M * g.kp <= busy * (g.kp > 48 << 10 ? g.kp : 48 << 10) && mx_few_fits(M, g.kp))
+    if (K > 0 && M * g.kp <= busy * (g.kp > 48 << 10 ? g.kp : 48 << 10) && mx_few_rows(M, N, g.kp, n_groups))
         return mx_few_packed({g, nullptr, 0, K, 0}, c_dtype, (hipStream_t)stream);
     return launch_gemm<MxRows>(g, c_dtype, (hipStream_t)stream);
 }
@@ -135,7 +135,7 @@ static size_t linear_code_bytes(int64_t M, int64_t K) {
 static bool linear_fused(int64_t M, int64_t N, int64_t K, int64_t n_groups) {
     const int64_t kp = mx_pad(K), busy = n_groups < M ? n_groups : M;
     if (M <= 0 || K <= 0) return false;
-    if (n_groups) return M * kp <= busy * (kp > 8192 ? kp : 8192) && mx_few_fits(M, kp);
+    if (n_groups) return M * kp <= busy * (kp > 8192 ? kp : 8192) && mx_few_rows(M, N, kp, n_groups);
     return mx_few_dense(M, N, kp) && (M <= 2 || mx_few_quantized(M, N, kp) <= 48 << 10);
 }
 
