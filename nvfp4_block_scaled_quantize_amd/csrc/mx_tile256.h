@@ -362,10 +362,15 @@ __global__ __launch_bounds__(256, 1) void k_mx_tile256(MxKindArgs<KIND> args, un
             const int64_t m0 = cur.m0 + wm * 128;
             const int left = cur.cols - wn * 64;
             const int64_t c0 = cur.n0 + wn * 64;
+            int el = lane;
+            // Grouped: opaque, so that addresses are made here and not held while the tiles multiply, for which there are
+            // no registers: what went to scratch memory was waited for together with all stores and the next tile's loads
+            // (16384 x 6144 x 2048 over 8 groups with the packed copy 306 us, was 320; with the checkpoint 367, was 384).
+            if constexpr (MODE == MxRows) asm volatile("" : "+v"(el));
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float16v gate[2] = {acc[i][0], acc[i][1]}, up[2] = {acc[i][2], acc[i][3]};
-                forward_rows<T, ACT, 2>(args, gate, up, piece, m0 + i * 32, cur.rows - wm * 128 - i * 32, c0, left, whole, lane);
+                forward_rows<T, ACT, 2>(args, gate, up, piece, m0 + i * 32, cur.rows - wm * 128 - i * 32, c0, left, whole, el);
                 __builtin_amdgcn_sched_barrier(0);
             }
         } else {
