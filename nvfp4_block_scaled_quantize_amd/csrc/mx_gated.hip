@@ -32,7 +32,7 @@ static int launch_forward(const MxFfnArgs& f, int dtype, int act, hipStream_t st
 // gets a second workgroup (17 x 4096 x 4096, 256 workgroups, 7.5 us against 11.6 by tiles, 256 x 512 x 4096 6.6
 // against 11.2; but 77 x 4999 x 2056, 471, 11.0 against 9.3, 64 x 9216 x 4096, 576, 25 against 13).  Groups: up to 48
 // Ki elements of A a group, or a row (1536 x 2048, 17 groups: 80 rows 13.6 against 14.2, 400 over 29 groups 20.6
-// against 23.4, 800 24.9 against 24.1).
+// against 23.4, 800 24.9 against 24.1).  (A group: on average.  Which of them hold rows is known on the device alone.)
 static bool few_packed(int64_t M, int64_t N, int64_t K, int64_t n_groups) {
     const int64_t kp = mx_pad(K), busy = n_groups < M ? n_groups : M;
     if (M <= 0 || N <= 0 || K <= 0) return false;
@@ -54,16 +54,25 @@ static bool few_fused(int64_t M, int64_t N, int64_t K, int64_t n_groups) {
 // or up to 800 workgroups of 32 x 32 (300 x 1500 x 1000, 470 of them, 6.2 us against 12.7, 700 x 777 x 1300, 550, 10.3
 // against 13.4, 1000 x 777 x 489, 800, 9.6 against 11.7; but 512 x 2048 x 2048, 1024, 12.7 against 11.5).  Groups: up
 // to 48 Ki elements of dY a group, or a row (400 rows over 29 groups, 1536 x 2048, 16.0 against 19.5; 600 over 15, 77
-// Ki, 15.4 against 13.7), or up to 1024 such workgroups (1000 x 600 x 700 over 6 groups, 703, 7.0 against 11.8).  Longer
-// rows gain less: 512 x 1024 x 8192, 512 of them, 19.8 against 21.7, 1000 x 800 over 6 groups, 925, K = 1024 9.8
-// against 12.1, K = 4096 18.7 against 17.6.  (The forward on as few of these in groups wins at short rows alone: 3000 x
-// 100 x 300 over 10 5.2 against 6.7, 5000 x 64 x 4096 over 12 18.1 against 12.3.)
+// Ki, 15.4 against 13.7), or up to 1024 such workgroups (1000 x 600 x 700 over 6 groups, 703, 7.0 against 11.8; 600 x
+// 1024 x 2048 over 12, 960, 13.0 either way).  Of either only where workgroups (of groups: the usual number, half of
+// the last ones full) times K are below 2.5 Mi, or 2.25 Mi: longer rows take more of a compute unit's LDS, so that from
+// K = 4096 on two workgroups of it run at once, at 8192 one, while tiles gain.  Dense 2000 x 300 x 4096, 630 of them,
+// 15.4 against 18.6, but 1000 x 800 x 4096, 800, 18.6 against 17.7, 600 x 1024 x 8192, 608, 27.7 against 22.5; 300 x
+// 1500 x 4096 over 4 groups, 517, 15.1 against 18.4, 350 x 473 x 7017 over 16, 270, 12.6 against 22.5, but 512 x 1024 x
+// 4096 over 4, 576, 19.1 against 16.6, 1000 x 800 over 6, 850, K = 2048 13.1 against 14.2, K = 4096 18.8 against 17.7, K =
+// 8192 38.9 against 24.4.  (The forward on as few of these in groups wins at short rows alone: 3000 x 100 x 300
+// over 10 5.2 against 6.7, 5000 x 64 x 4096 over 12 18.1 against 12.3.)
 static bool few_backward(int64_t M, int64_t N, int64_t K, int64_t n_groups) {
     const int64_t kp = mx_pad(K), busy = n_groups < M ? n_groups : M, cols = (N + 31) / 32;
     if (M <= 0 || N <= 0 || K <= 0) return false;
-    if (n_groups)
-        return (M * kp <= busy * (kp > 48 << 10 ? kp : 48 << 10) || (M / 32 + busy) * cols <= 1024) && mx_few_rows(M, N, kp, n_groups);
-    return mx_few_dense(M, N, kp) || ((M + 31) / 32 * cols <= 800 && mx_few_two_fit(M, kp));
+    if (n_groups) {
+        const int64_t most = (M / 32 + busy) * cols, usual = (2 * (M / 32) + busy) / 2 * cols;
+        return (M * kp <= busy * (kp > 48 << 10 ? kp : 48 << 10) || (most <= 1024 && usual * kp < 9 << 18)) &&
+               mx_few_rows(M, N, kp, n_groups);
+    }
+    const int64_t workgroups = (M + 31) / 32 * cols;
+    return mx_few_dense(M, N, kp) || (workgroups <= 800 && workgroups * kp < 5 << 19 && mx_few_two_fit(M, kp));
 }
 
 // Extents as in mxfp4_gemm, for a product of 2 N columns.
