@@ -111,6 +111,14 @@ class MX8Tensor:
             self._views()
         return self._scales
 
+    @codes.setter
+    def codes(self, value):
+        self._scales, self._codes, self._data = self.scales, value, None
+
+    @scales.setter
+    def scales(self, value):
+        self._codes, self._scales, self._data = self.codes, value, None
+
     @property
     def shape(self):
         return (*(self.codes.shape[:-1] if self._data is None else self._lead), self.k)
