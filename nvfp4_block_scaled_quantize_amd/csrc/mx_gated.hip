@@ -12,8 +12,10 @@ namespace nvfp4 {
 // small ones run beside each other's products): 512 small ones take 55, up to 256 of them 37.  8192 x 9216 x 4096
 // 318 us against 345 with small ones, 4096 x 4096 x 8192 132 against 148, 8192 x 2048 x 2048 44 against 46; but
 // 2048 x 9216 x 4096 (576 large tiles) 115 against 92.  Where rows are grouped a large tile's ends cost a little
-// more: 32768 rows over 8 groups, 4608 x 4096, 700 against 736, 16384 over 4 groups, 2048 x 4096, 179 against 167,
-// 8191 over 15 of 16 groups, 1536 x 2048, 59 against 43.  float32 H is left to the small ones.
+// more: H over 8 groups, 32768 rows, 4608 x 4096, 747 against 794, over 2, 8192, 9216 x 4096, 391 against 403; over 4, 16384,
+// 2048 x 4096, 190 against 188 (and the packed copy 193 against 179), 8191 over 15 of 16, 1536 x 2048, 52 against 47.  (Few
+// rows in each of many groups it judges a little too well for the small ones: 16384 over 60 of 64, 4096 x 2048, 290,
+// 277 with large ones.)  float32 H is left to the small ones: 8192 x 9216 x 4096 375, with large ones 345.
 static int launch_forward(const MxFfnArgs& f, int dtype, int act, hipStream_t st) {
     const MxGArgs& g = f.g;
     const int mode = g.n_groups ? MxRows : MxDense;
@@ -22,7 +24,7 @@ static int launch_forward(const MxFfnArgs& f, int dtype, int act, hipStream_t st
         if (mode == MxRows) m = (2 * g.M / side + (g.n_groups < g.M ? g.n_groups : g.M) + 1) / 2;
         return m * ((2 * g.N + side - 1) / side);
     };
-    const int64_t big = (tiles(256) + 255) / 256 * (mode == MxRows ? 104 : 100), n = tiles(128), rest = n % 512;
+    const int64_t big = (tiles(256) + 255) / 256 * (mode == MxRows ? 102 : 100), n = tiles(128), rest = n % 512;
     const int64_t small = n / 512 * 55 + (rest == 0 ? 0 : rest <= 256 ? 37 : 55);
     if (dtype == NVFP4_BF16 && big <= small) return mx_forward256(f, mode, act, st);
     return mx_forward128(f, mode, dtype, act, st);
