@@ -9,7 +9,8 @@
 //
 // From a checkpoint it is 33/32 bytes read, and as many instructions as the vector units do meanwhile: 8192 x 4096
 // both copies 22 us (the same of bfloat16 29), the row copy 10, the column copy 12, against floors of 10, 7 and 7;
-// 8192 x 9216 49, 22 and 30.
+// 8192 x 9216 49, 22 and 30.  Stochastic, eight checkpoints and their copies in turn: 8192 x 9216 both copies 75 against
+// 49 to nearest there, 36 against 23 and 45 against 31; 8192 x 4096 38 against 25; 8191 x 1536 in 15 groups 22 against 11.
 //
 // Stochastic rounding of bfloat16 is bound by the vector units instead (busy in 0.84 of the
 // cycles, in 0.42 to nearest): ten Philox rounds per eight elements and copy, and a conversion

@@ -23,7 +23,7 @@
 //
 // Backward: a tile of dH, whose epilogue reads the checkpoint and writes dG, dU and H.  8192 x 9216 x 4096 280
 // us, 260 without H; 4096 x 9216 x 4096 139; 8192 x 4096 x 2048 85 (a bfloat16 dH on large tiles and a kernel that
-// reads it: 287, 160 and 104).  With nothing stored it takes 215, without the checkpoint's loads 213, without
+// reads it: 287, 160 and 104).  In float32 398, without H 348 (906 and 604 MB written); 8192 x 4096 x 2048 114.  With nothing stored it takes 215, without the checkpoint's loads 213, without
 // the epilogue 161: what goes to and from memory (156 and 453 MB, 87 us at the rates of plain reads and
 // writes) adds to the product's time instead of hiding beside it, whichever way it is asked for.  Slower
 // or no faster: 256 x 256 tiles (291), the checkpoint loaded straight into LDS as another stage of codes (282), its
