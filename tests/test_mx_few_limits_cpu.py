@@ -16,7 +16,8 @@ SIZES = [(1, 1 << 28, 128, 0), (2, (1 << 28) + 5, 40, 0), (8192, 65536, 128, 819
 @pytest.mark.parametrize("M,N,K,groups", SIZES)
 def test_workspaces_of_the_layers(nv, M, N, K, groups):  # noqa: F811
     """They are quantized by a kernel of their own, into a workspace."""
-    for f in (nv.mxfp4_linear_workspace_bytes, nv.mxfp4_gated_linear_workspace_bytes):
+    lib = nv.load_library()
+    for f in (lib.mxfp4_linear_workspace_bytes, lib.mxfp4_gated_linear_workspace_bytes):
         assert f(M, N, K, groups) >= M * 17 * 4
         assert f(M, 1000, K, 0) == 0 or M > 2     # where the few rows' kernel fits, it quantizes them
 
